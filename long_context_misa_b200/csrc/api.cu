@@ -9,21 +9,10 @@
 
 #include <cuda.h>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_common.h"
 #include "internal.h"
 
 namespace {
-
-// One NVTX range per library call that launches work, named after the entry
-// point, so that a profiler's timeline shows each call around its kernels.
-// Without a profiler attached the calls are no-ops.
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange &) = delete;
-  NvtxRange &operator=(const NvtxRange &) = delete;
-};
 
 thread_local char g_err[512] = "";
 std::atomic<int> g_fail_next{0};
@@ -39,24 +28,10 @@ std::atomic<int> g_fail_next{0};
 std::atomic<int> g_select_in_kernel{0};
 std::atomic<void *> g_ev_start{nullptr}, g_ev_stop{nullptr};
 
-// Launch the scoring kernel, bracketed by the profiling events when set.
-template <class F>
-cudaError_t timed_scoring(cudaStream_t stream, F &&launch) {
-  void *a = g_ev_start.load(), *b = g_ev_stop.load();
-  // External records: inside a stream capture they become event-record nodes
-  // that stamp the time on every graph launch.
-  unsigned flags = 0;
-  if (a && b) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive)
-      flags = cudaEventRecordExternal;
-    cudaError_t e = cudaEventRecordWithFlags(static_cast<cudaEvent_t>(a), stream, flags);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = launch();
-  if (e == cudaSuccess && a && b) e = cudaEventRecordWithFlags(static_cast<cudaEvent_t>(b), stream, flags);
-  return e;
-}
+}  // namespace
+
+namespace misa {
+namespace api {
 
 misa_status fail(misa_status st, const char *fmt, ...) {
   va_list ap;
@@ -82,6 +57,32 @@ bool injected_failure(const char *where, misa_status *st) {
     }
   }
   return false;
+}
+
+}  // namespace api
+}  // namespace misa
+
+namespace {
+
+using namespace misa::api;
+
+// Launch the scoring kernel, bracketed by the profiling events when set.
+template <class F>
+cudaError_t timed_scoring(cudaStream_t stream, F &&launch) {
+  void *a = g_ev_start.load(), *b = g_ev_stop.load();
+  // External records: inside a stream capture they become event-record nodes
+  // that stamp the time on every graph launch.
+  unsigned flags = 0;
+  if (a && b) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive)
+      flags = cudaEventRecordExternal;
+    cudaError_t e = cudaEventRecordWithFlags(static_cast<cudaEvent_t>(a), stream, flags);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e = launch();
+  if (e == cudaSuccess && a && b) e = cudaEventRecordWithFlags(static_cast<cudaEvent_t>(b), stream, flags);
+  return e;
 }
 
 misa_status check_cache(const misa_cache *c, bool need_pool) {

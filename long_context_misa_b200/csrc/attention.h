@@ -1,0 +1,56 @@
+// Host-side launchers and device views of the attention side
+// (misa_attention.h), shared between its translation units.
+#pragma once
+
+#include "common.cuh"
+#include "misa_attention.h"
+
+namespace misa {
+
+// Device view of the caller's attention cache (by value).
+struct KvView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int32_t *seq_len;
+  uint32_t *status;
+  int n_seq, L_cap, H_kv, d, fp8;
+};
+
+__device__ __forceinline__ void flag(const KvView &c, uint32_t bit) {
+  if (c.status) atomicOr(c.status, bit);
+}
+
+// Rotary parameters of a launch.
+struct RopeView {
+  const uint64_t *phase;  // nullptr: no rotation
+  int rot, first, interleaved;
+  float amplitude;
+};
+
+// rope.cu
+cudaError_t launch_rope(const RopeView &r, const misa_rope_rows *groups, int n_groups, cudaStream_t s);
+
+// kvcache.cu
+cudaError_t launch_append_kv(const KvView &c, const misa_new_kv &in, const int32_t *new_pos, int count,
+                             const RopeView &r, const int32_t *rope_pos, bool commit, cudaStream_t s);
+cudaError_t launch_read_kv(const KvView &c, const int32_t *seq, const int32_t *tok, int n, int k, uint16_t *k_out,
+                           uint16_t *v_out, cudaStream_t s);
+
+// attend.cu
+struct AttendView {
+  const uint16_t *q;
+  const int32_t *q_seq, *q_pos;
+  int n_q, H;
+  float scale;
+  const int32_t *topk;  // nullptr: whole prefixes
+  int k;
+  const int32_t *draft_start;  // nullptr: no drafted tokens
+  const uint32_t *draft_mask;
+  int n_draft;
+  uint16_t *out;
+  float *lse;
+};
+size_t attend_ws_bytes(const KvView &c, int n_q, int H, int k, int n_draft);
+cudaError_t launch_attend(const KvView &c, const AttendView &a, void *ws, cudaStream_t s);
+
+}  // namespace misa

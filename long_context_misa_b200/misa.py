@@ -206,14 +206,20 @@ class Queries:
 
 
 class Workspace:
-    """Grow-only device scratch buffer for the calls that need one."""
+    """Grow-only device scratch buffer for the calls that need one.
+
+    A buffer that was outgrown stays allocated: a captured graph may still
+    hold its address."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
+        self.outgrown = []
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
+            if self.buf.numel():
+                self.outgrown.append(self.buf)
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         return self.buf
 

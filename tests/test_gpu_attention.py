@@ -1,0 +1,709 @@
+"""GPU tests of the attention side against plain implementations in 64 bits.
+
+Tolerances.  A rounding to a type is off by at most half a step: 2^-8 of the
+value for bf16, 2^-11 for f16, 2^-24 for fp32, 2^-4 for e4m3 (half a step of
+its subnormals, 2^-10, below 2^-6).
+
+Rotary rows: one bf16 rounding, and fp32 arithmetic on cos and sin that are
+right to 2 units (2^-23 each) with a rounded product and sum, at most
+4 * 2^-23 of |a| + |b|.
+
+Attention: with E = scale * max_t sum_e |q_e k_te| every logit is off by at
+most (d + 8) 2^-23 E (a sum of d products in fp32, however it is ordered and
+whether it is rounded or truncated, and the factors after it) plus 2^-22 of
+the largest |logit| + 1 for the base-2 argument and exponential; call that
+delta.  The weights are then off by 2 delta + 2^-20 relatively (numerator and
+sum), and by their rounding to bf16 (2^-8) or f16 (2^-11, and 2^-25 of the
+largest weight below its normal range) before they meet the values, so with
+A = sum_t p_t |v_t| / sum_t p_t
+    |out - exact| <= 2^-8 |exact| + (rounding + 2 delta + 2^-20) A
+                     [+ 2^-25 max_t(p_t vs_t) sum_t |code_t| / sum_t p_t],
+    |lse - exact| <= delta + 2^-20 + 2^-23 |exact|.
+"""
+import math
+
+import pytest
+import torch
+
+from long_context_misa_b200 import attention as A
+from long_context_misa_b200 import misa as M
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF16 = 2.0 ** -8
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------- rotary
+
+def rope64(x, pos, r):
+    """Exact rotation of x [..., H, d] at pos [...], and |a| + |b| per element."""
+    x = x.double()
+    i = torch.arange(r.rot // 2, device=DEV)
+    ia, ib = ((r.first + i, r.first + r.rot // 2 + i) if r.layout == "half" else (r.first + 2 * i, r.first + 2 * i + 1))
+    # whole turns of the table's own 64-bit increments, in exact integers
+    turn = torch.tensor([[(int(p) * (int(f) % 2 ** 64)) % 2 ** 64 / 2 ** 64 for f in r.phases.tolist()]
+                         for p in pos.reshape(-1).tolist()], dtype=torch.float64, device=DEV)
+    t = (2 * math.pi * turn).view(*pos.shape, 1, -1)
+    a, b = x[..., ia], x[..., ib]
+    y, m = x.clone(), torch.zeros_like(x)
+    y[..., ia] = r.amplitude * (a * t.cos() - b * t.sin())
+    y[..., ib] = r.amplitude * (b * t.cos() + a * t.sin())
+    m[..., ia] = m[..., ib] = abs(r.amplitude) * (a.abs() + b.abs())
+    return y, m
+
+
+def check_rope(out, x, pos, r):
+    y, m = rope64(x, pos, r)
+    tol = BF16 * y.abs() + 4 * 2.0 ** -23 * m
+    assert bool(((out.double() - y).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot,first", [(128, 64, 0), (128, 64, 64), (128, 128, 0), (64, 32, 8), (128, 48, 16),
+                                         (96, 10, 3), (128, 2, 126), (40, 32, 8), (7, 6, 1), (192, 176, 8)])
+@pytest.mark.parametrize("n,H", [(1, 1), (37, 5)])
+def test_rope_rows(layout, d, rot, first, n, H):
+    g = gen(1)
+    r = A.Rope(rot, layout=layout, first=first, scaling="yarn", factor=4.0)
+    x = randn(g, n, H, d).bfloat16()
+    pos = torch.randint(0, 1 << 18, (n,), generator=g, device=DEV).int()
+    pos[0] = (1 << 18) - 1
+    out = torch.full_like(x, 7.0)
+    A.apply_rope(r, [(x, pos, out)])
+    check_rope(out, x, pos, r)
+    here = x.clone()
+    A.apply_rope(r, [(here, pos, here)])
+    assert torch.equal(here, out)
+
+
+def test_rope_groups_strides_and_negative_positions():
+    g = gen(2)
+    r = A.Rope(64, layout="half", first=32)
+    wide = randn(g, 50, 6, 3, 128).bfloat16()         # heads inside a fused projection
+    x = wide[:, :, 1]
+    odd = randn(g, 9, 3, 130).bfloat16()[:, :, 1:129]  # rows off 16 bytes
+    seqs = [(x, torch.arange(-25, 25, device=DEV).int()), (odd, ints([0, 1, -1, 5, 2 ** 31 - 1, -2 ** 31, 3, 4, 262143])),
+            (randn(g, 0, 4, 128).bfloat16(), ints([])), (randn(g, 2000, 40, 128).bfloat16(), torch.arange(2000, device=DEV).int())]
+    outs = [torch.empty_like(v) for v, _ in seqs]
+    A.apply_rope(r, [(v, p, o) for (v, p), o in zip(seqs, outs)])
+    for (v, p), o in zip(seqs[:2], outs):
+        check_rope(o, v, p, r)
+    check_rope(outs[3][::97], seqs[3][0][::97], seqs[3][1][::97], r)
+    before = wide.clone()
+    A.apply_rope(r, [(x, seqs[0][1], x)])             # in place inside the projection
+    check_rope(x, before[:, :, 1], seqs[0][1], r)
+    assert torch.equal(wide[:, :, 0], before[:, :, 0]) and torch.equal(wide[:, :, 2], before[:, :, 2])
+
+
+def test_rope_turns_back():
+    """Positions that differ by the same amount give the same products of rows (the point of a rotation)."""
+    g = gen(3)
+    r = A.Rope(128)
+    a, b = randn(g, 1, 1, 128).bfloat16(), randn(g, 1, 1, 128).bfloat16()
+    dots = []
+    for p in (0, 1000, 262000):
+        x = torch.cat([a, b])
+        A.apply_rope(r, [(x, ints([p + 13, p]), x)])
+        dots.append(float((x[0].double() * x[1].double()).sum()))
+    # each rotated element is off by 2^-8 of itself (and fp32 terms far below)
+    lim = 2 * 2.1 * BF16 * float(a.double().norm() * b.double().norm())
+    assert max(dots) - min(dots) <= lim
+
+
+# -------------------------------------------------------------------- cache
+
+def plain_codes(x):
+    """The cache's quantisation rule on fp32 rows, on the CPU."""
+    x = x.float().cpu()
+    amax = x.abs().amax(-1)
+    sc = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+    return (x / sc[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV), sc.to(DEV)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,H_kv", [(128, 8), (128, 1), (64, 3)])
+@pytest.mark.parametrize("count", [1, 7, 300])
+def test_append_plain(e4m3, d, H_kv, count):
+    g = gen(4)
+    kv = A.KVCache.empty(3, 512, H_kv, d, e4m3)
+    for t in (kv.k, kv.v):
+        t.fill_(33 if e4m3 else 33.0)
+    k, v = (randn(g, 3, count, H_kv, d).bfloat16() for _ in range(2))
+    k[0, 0, 0] = 0                                     # a zero row
+    pos = ints([5, -1, 512 - count])
+    A.append_kv(kv, k, v, pos)
+    assert kv.device_status() == 0
+    assert kv.seq_len.tolist() == [5 + count, 0, 512]
+    for new, rows, sc in ((k, kv.k, kv.k_scale), (v, kv.v, kv.v_scale)):
+        want, scale = plain_codes(new) if e4m3 else (new, None)
+        for s, p in ((0, 5), (2, 512 - count)):
+            assert torch.equal(rows[s, p:p + count], want[s])
+            if e4m3:
+                assert torch.equal(sc[s, p:p + count], scale[s])
+        keep = torch.ones(3, 512, dtype=torch.bool)
+        keep[0, 5:5 + count] = keep[2, 512 - count:] = False
+        assert bool((rows[keep.to(DEV)] == 33).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot,first", [(128, 128, 0), (128, 64, 64), (128, 32, 8), (128, 10, 3), (64, 64, 0), (64, 6, 58)])
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_append_rotated(layout, d, rot, first, e4m3):
+    g = gen(5)
+    r = A.Rope(rot, layout=layout, first=first)
+    n, count, H_kv = 2, 19, 4
+    kv = A.KVCache.empty(n, 262144 if d == 64 else 64, H_kv, d, e4m3)
+    fused = randn(g, n, count, 2, H_kv, d).bfloat16()  # keys and values of one projection
+    k, v = fused[:, :, 0], fused[:, :, 1]
+    pos = ints([3, kv.L_cap - count])
+    at = pos[:, None] + torch.arange(count, device=DEV).int()
+    for given in (None, (at * 3 - 50).contiguous()):
+        A.append_kv(kv, k, v, pos, rope=r, rope_pos=given, commit=given is None)
+        y, m = rope64(k, at if given is None else given, r)
+        for s in range(n):
+            p = int(pos[s])
+            rows = kv.k[s, p:p + count]
+            exact, mix = y[s], m[s]
+            fp32 = 4 * 2.0 ** -23 * mix
+            if e4m3:
+                sc = kv.k_scale[s, p:p + count].double()
+                top = exact.abs().amax(-1)
+                # amax carries its element's fp32 error, the quotient one rounding
+                assert bool(((sc - top / 448).abs() <= (fp32.amax(-1) + 2.0 ** -23 * top) / 448).all())
+                got = rows.view(torch.float8_e4m3fn).double() * sc[..., None]
+                step = torch.maximum(2.0 ** -4 * exact.abs(), 2.0 ** -10 * sc[..., None])
+                assert bool(((got - exact).abs() <= step * (1 + 2.0 ** -18) + 2 * fp32 + 2.0 ** -22 * top[..., None]).all())
+            else:
+                assert bool(((rows.double() - exact).abs() <= BF16 * exact.abs() + fp32).all())
+            want = plain_codes(v[s])[0] if e4m3 else v[s]
+            assert torch.equal(kv.v[s, p:p + count], want)
+    assert kv.seq_len.tolist() == [3 + count, kv.L_cap]
+
+
+def test_append_past_the_end_and_special_values():
+    g = gen(6)
+    kv = A.KVCache.empty(3, 16, 2, 64, True)
+    k, v = (randn(g, 3, 4, 2, 64).bfloat16() for _ in range(2))
+    k[0, 1, 0, 5] = math.nan
+    v[0, 2, 1, 7] = math.inf
+    A.append_kv(kv, k, v, ints([0, 13, 2 ** 31 - 1]))
+    assert kv.device_status() == M.DEV_APPEND_RANGE
+    assert kv.seq_len.tolist() == [4, 0, 0]
+    assert not bool(kv.k[1:].any()) and not bool(kv.v[1:].any())
+    read_k = kv.k.view(torch.float8_e4m3fn).float()[0, :4]
+    assert bool(torch.isnan(read_k[1, 0, 5])) and int(torch.isnan(read_k).sum()) == 1
+    read_v = kv.v.view(torch.float8_e4m3fn).float()[0, :4] * kv.v_scale[0, :4, :, None]
+    assert not bool(torch.isfinite(read_v[2, 1, 7]))
+    assert bool(torch.isfinite(read_v[3]).all())
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,H_kv", [(128, 8), (64, 1), (64, 5)])
+def test_read_back(e4m3, d, H_kv):
+    g = gen(7)
+    kv = A.KVCache.empty(3, 100, H_kv, d, e4m3)
+    k, v = (randn(g, 3, 100, H_kv, d).bfloat16() for _ in range(2))
+    A.append_kv(kv, k, v, ints([0, 0, 0]))
+    tok = torch.randint(-1, 100, (4, 33), generator=g, device=DEV).int()
+    tok[1, 3:6] = 7                                    # the same token three times
+    seq = ints([2, 0, 0, 1])
+    ko, vo = A.read_kv(kv, seq, tok)
+    assert kv.device_status() == 0
+    for out, rows, sc in ((ko, kv.k, kv.k_scale), (vo, kv.v, kv.v_scale)):
+        x = (rows.view(torch.float8_e4m3fn).float() * sc[..., None]) if e4m3 else rows.float()
+        want = x[seq.long()[:, None], tok.long().clamp_min(0)].bfloat16()
+        want[tok < 0] = 0
+        assert torch.equal(out, want)
+    bad = ints([[0, 100, 2 ** 31 - 1], [-2, 5, -1]])
+    ko, vo = A.read_kv(kv, ints([0, 3]), bad)
+    assert kv.device_status() == M.DEV_BAD_POSITION
+    assert torch.equal(ko[0, 0], A.read_kv(kv, ints([0]), ints([[0]]))[0][0, 0])
+    assert not bool(ko[0, 1:].any()) and not bool(ko[1].any()) and not bool(vo[0, 1:].any()) and not bool(vo[1].any())
+    only = torch.empty(1, 1, H_kv, d, dtype=torch.bfloat16, device=DEV)
+    st = torch.cuda.current_stream().cuda_stream
+    import ctypes
+    assert M._lib.misa_read_kv(ctypes.byref(kv.struct), seq.data_ptr(), ints([[7]]).data_ptr(), 1, 1, None,
+                               only.data_ptr(), st) == 0
+    assert torch.equal(only, A.read_kv(kv, seq[:1], ints([[7]]))[1])
+
+
+# ---------------------------------------------------------------- attention
+
+class Case:
+    """Random cache, queries, lists and drafted trees; everything nobody sees can be poisoned."""
+
+    def __init__(self, e4m3=True, d=128, H_kv=2, G=4, lens=(300, 77), per=(1, 1), k=0, drafts=0, seed=0, causal=False,
+                 spread=1.0, slack=40):
+        g = self.g = gen(seed)
+        self.e4m3, self.d, self.H_kv, self.G, self.lens, self.drafts = e4m3, d, H_kv, G, lens, drafts
+        n_seq, cap = len(lens), max(lens) + drafts + slack
+        self.cap = cap
+        if e4m3:
+            codes = [torch.randint(0, 127, (n_seq, cap, H_kv, d), generator=g, device=DEV) +
+                     128 * torch.randint(0, 2, (n_seq, cap, H_kv, d), generator=g, device=DEV) for _ in range(2)]
+            self.k, self.v = (c.to(torch.uint8) for c in codes)
+            self.ks, self.vs = (torch.exp(spread * randn(g, n_seq, cap, H_kv)) / 200 for _ in range(2))
+        else:
+            self.k, self.v = (randn(g, n_seq, cap, H_kv, d).bfloat16() for _ in range(2))
+            self.ks = self.vs = None
+        self.kv = A.KVCache(self.k, self.v, self.ks, self.vs, ints(lens))
+        seq = [s for s, n in enumerate(per) for _ in range(n)]
+        pos = [lens[s] - 1 - (per[s] - 1 - i if causal else 0) for s in range(n_seq) for i in range(per[s])]
+        self.seq, self.pos = seq, [max(p, -1) for p in pos]
+        self.n = len(seq)
+        self.q = randn(g, self.n, H_kv * G, d).bfloat16()
+        self.topk = None
+        if k:
+            rows = []
+            for s, p in zip(seq, self.pos):
+                t = torch.randperm(p + 1, generator=g, device=DEV)[:k] if p >= 0 else ints([])
+                t = t.int().sort().values
+                rows.append(torch.cat([t, torch.full((k - t.numel(),), -1, dtype=torch.int32, device=DEV)]))
+            self.topk = torch.stack(rows) if rows else torch.empty(0, k, dtype=torch.int32, device=DEV)
+        self.draft = None
+        if drafts:
+            cg = torch.Generator().manual_seed(seed)
+            masks = []
+            for s in range(n_seq):
+                par = [int(torch.randint(-1, j, (1,), generator=cg)) if j else -1 for j in range(drafts)]
+                m = A.tree_mask(par, drafts)
+                masks += [m[i % drafts] for i in range(per[s])]
+            self.mask = torch.stack(masks).to(DEV) if masks else torch.empty(0, -(-drafts // 32), dtype=torch.int32, device=DEV)
+            self.start = ints([x + 3 for x in lens])
+            self.draft = A.Draft(self.start, self.mask, drafts)
+
+    def queries(self, scale=None):
+        return A.AttentionQueries(self.q, ints(self.seq), ints(self.pos), scale)
+
+    def sees(self, i):
+        """Tokens that query i sees (with repetitions)."""
+        s, p = self.seq[i], min(self.pos[i], self.lens[self.seq[i]] - 1)
+        if self.topk is None:
+            t = list(range(p + 1))
+        else:
+            t = [x for x in self.topk[i].tolist() if 0 <= x <= p]
+        if self.draft is not None:
+            w = self.mask[i].tolist()
+            t += [int(self.start[s]) + j for j in range(self.drafts) if (w[j // 32] >> (j % 32)) & 1]
+        return t
+
+    def poison(self):
+        """NaN and infinities in every row that no query sees."""
+        seen = torch.zeros(len(self.lens), self.cap, dtype=torch.bool, device=DEV)
+        for i in range(self.n):
+            t = self.sees(i)
+            if t:
+                seen[self.seq[i], torch.tensor(t, device=DEV)] = True
+        self._spoil(~seen)
+
+    def _spoil(self, where):
+        for x, s in ((self.k, self.ks), (self.v, self.vs)):
+            if self.e4m3:
+                x[where] = 0x7F
+                s[where] = math.nan
+                s.view(-1)[::2] = torch.where(where.reshape(-1)[:, None].expand(-1, self.H_kv).reshape(-1)[::2],
+                                              math.inf, s.view(-1)[::2])
+            else:
+                x[where] = math.inf
+                x[..., ::3] = torch.where(where[..., None, None], math.nan, x[..., ::3])
+
+    def rows64(self, i):
+        s, t = self.seq[i], torch.tensor(self.sees(i), dtype=torch.long, device=DEV)
+        out = []
+        for x, sc in ((self.k, self.ks), (self.v, self.vs)):
+            if self.e4m3:
+                c = x[s][t].view(torch.float8_e4m3fn).double()
+                out.append((c, sc[s][t].double()))
+            else:
+                out.append((x[s][t].double(), torch.ones(t.numel(), self.H_kv, dtype=torch.float64, device=DEV)))
+        return out
+
+    def check(self, out, lse, scale=None, only=None):
+        scale = self.d ** -0.5 if scale is None else scale
+        for i in range(self.n) if only is None else only:
+            (kc, ks), (vc, vs) = self.rows64(i)
+            q = self.q[i].double().view(self.H_kv, self.G, self.d)
+            o, l_ = out[i].double().view(q.shape), lse[i].double().view(q.shape[:2])
+            if kc.shape[0] == 0:
+                assert bool((o == 0).all()) and bool((l_ == -math.inf).all())
+                continue
+            k = kc * ks[..., None]
+            s = torch.einsum("hgd,thd->hgt", q, k) * scale
+            E = (torch.einsum("hgd,thd->hgt", q.abs(), k.abs()) * abs(scale)).amax(-1)
+            delta = (self.d + 8) * 2.0 ** -23 * E + 2.0 ** -22 * (s.abs().amax(-1) + 1)
+            m = s.amax(-1, keepdim=True)
+            p = torch.exp(s - m)
+            tot = p.sum(-1)
+            exact = torch.einsum("hgt,thd->hgd", p, vc * vs[..., None]) / tot[..., None]
+            mass = torch.einsum("hgt,thd->hgd", p, vc.abs() * vs[..., None]) / tot[..., None]
+            e_lse = m[..., 0] + torch.log(tot)
+            rounding = 2.0 ** -11 if self.e4m3 else BF16
+            tol = BF16 * exact.abs() + (rounding + 2 * delta[..., None] + 2.0 ** -20) * mass
+            if self.e4m3:
+                w = (p * vs.t()[:, None, :]).amax(-1)
+                tol = tol + 2.0 ** -25 * (w / tot)[..., None] * vc.abs().sum(0)[:, None, :]
+            bad = ~((o - exact).abs() <= tol)
+            assert not bool(bad.any()), (i, int(bad.sum()), float((o - exact).abs().max()), float(tol.min()))
+            off = (l_ - e_lse).abs()
+            assert bool((off <= delta + 2.0 ** -20 + 2.0 ** -23 * e_lse.abs()).all()), (i, float(off.max()))
+
+    def run(self, scale=None, check=True, **kw):
+        out, lse = A.attend(self.kv, self.queries(scale), topk=self.topk, draft=self.draft, with_lse=True, **kw)
+        if check:
+            self.check(out, lse, scale)
+        return out, lse
+
+
+TYPES = [(True, 128), (False, 128), (True, 64), (False, 64)]
+
+
+@pytest.mark.parametrize("e4m3,d", TYPES)
+@pytest.mark.parametrize("H_kv,G", [(1, 1), (2, 4), (3, 7), (1, 16), (1, 24), (2, 40), (1, 128)])
+def test_selected(e4m3, d, H_kv, G):
+    c = Case(e4m3, d, H_kv, G, lens=(300, 1, 77), per=(2, 1, 3), k=100, causal=True, seed=11)
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3,d", TYPES)
+@pytest.mark.parametrize("H_kv,G", [(1, 1), (2, 4), (3, 7), (1, 16), (2, 40), (1, 128)])
+def test_whole_prefixes(e4m3, d, H_kv, G):
+    c = Case(e4m3, d, H_kv, G, lens=(300, 1, 77), per=(9, 1, 3), causal=True, seed=12)
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3,d", TYPES)
+@pytest.mark.parametrize("drafts", [1, 5, 31, 32, 33, 70])
+@pytest.mark.parametrize("k", [0, 50])
+def test_drafted_trees(e4m3, d, drafts, k):
+    c = Case(e4m3, d, 2, 3, lens=(130, 40, 5), per=(drafts, min(3, drafts), drafts), k=k, drafts=drafts, seed=13)
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("k", [1, 2, 15, 16, 17, 31, 33, 255, 256, 257, 2048, 5000])
+def test_list_lengths(e4m3, k):
+    c = Case(e4m3, 128, 2, 4, lens=(6000, 40), per=(2, 1), k=k, seed=k)
+    c.poison()
+    c.run()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 32, 33, 127, 129, 4097, 20001])
+def test_prefix_lengths(e4m3, L):
+    c = Case(e4m3, 128, 1, 5, lens=(L,), per=(3,), seed=L)
+    c.poison()
+    c.run()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("drafts", [0, 24])
+def test_many_rows_share_a_prefix(e4m3, drafts):
+    """Rows of many queries of one sequence, more than a tile."""
+    c = Case(e4m3, 128, 2, 8, lens=(500, 1300), per=(24, 19), drafts=drafts, causal=drafts == 0, seed=21)
+    c.poison()
+    c.run()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("k", [0, 20])
+def test_rows_that_see_nothing(e4m3, k):
+    c = Case(e4m3, 128, 2, 4, lens=(50, 20, 30), per=(2, 2, 2), k=k, drafts=3, seed=31)
+    c.pos = [-1, 49, 19, -1, 29, 29]
+    c.mask[0] = 0                                      # neither prefix nor drafts
+    c.mask[4] = 0
+    if k:
+        c.topk[4] = -1                                 # a list of nothing
+    c.poison()
+    out, lse = c.run()
+    assert not bool(out[0].any()) and bool((lse[0] == -math.inf).all())
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_empty_sequence_and_empty_batch(e4m3):
+    c = Case(e4m3, 64, 2, 2, lens=(10, 10), per=(1, 1), seed=32)
+    c.kv.seq_len[1] = 0
+    c.lens, c.pos = (10, 0), [9, -1]
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+    e = Case(e4m3, 64, 2, 2, lens=(10,), per=(0,), seed=33)
+    out, lse = e.run()
+    assert out.shape[0] == 0 and lse.shape[0] == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_lists_in_any_order_with_repeats_and_strangers(e4m3):
+    c = Case(e4m3, 128, 2, 4, lens=(300, 200), per=(1, 2), k=64, seed=34)
+    g = c.g
+    c.topk = torch.randint(-1, 300, (3, 64), generator=g, device=DEV).int()
+    c.topk[0, 5] = c.topk[0, 60] = 17                  # counts twice
+    c.topk[1, ::3] = -1
+    c.topk[2, 1] = 2 ** 31 - 1
+    c.topk[2, 2] = -2 ** 31
+    c.pos[2] = 50                                      # tokens 51.. of its list are outside its prefix
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("k", [0, 30])
+def test_queries_outside_the_cache(e4m3, k):
+    c = Case(e4m3, 128, 1, 3, lens=(60, 40), per=(2, 2), k=k, drafts=2, seed=35)
+    want, wl = c.run()
+    seq, pos = ints([0, 2, -1, 1]), ints([59, 5, 5, -7])
+    out, lse = A.attend(c.kv, A.AttentionQueries(c.q, seq, pos), topk=c.topk, draft=c.draft, with_lse=True)
+    assert c.kv.device_status() == M.DEV_BAD_POSITION
+    # the same query may run in another split or tile: same tokens, other order of sums
+    c.check(out, lse, only=[0])
+    assert not bool(out[1:].any()) and bool((lse[1:] == -math.inf).all())
+    c.kv.status.zero_()
+    out, lse = A.attend(c.kv, A.AttentionQueries(c.q, ints(c.seq), ints([59, 60, 39, 39])), topk=c.topk, draft=c.draft,
+                        with_lse=True)
+    assert c.kv.device_status() == M.DEV_BAD_POSITION  # clamped to the sequence
+    if k == 0:
+        c.check(out, lse)
+
+
+def test_drafts_outside_the_cache():
+    c = Case(True, 128, 1, 3, lens=(60, 40), per=(3, 3), drafts=3, seed=36, slack=0)
+    c.start.copy_(ints([c.cap - 2, -1]))               # slot 2 of sequence 0 and slot 0 of sequence 1 are outside
+    for topk in (None, ints([[1, 2, 3, -1]] * 6)):
+        c.topk = topk
+        c.kv.status.zero_()
+        c.mask.copy_(ints([[0b011]] * 3 + [[0b110]] * 3))
+        c.run()
+        assert c.kv.device_status() == 0
+        c.mask[2] = 0b111
+        keep = c.mask.clone()
+        out, lse = c.run(check=False)
+        assert c.kv.device_status() == M.DEV_BAD_POSITION
+        c.mask[2] = 0b011                              # what is outside is not seen
+        c.check(out, lse)
+        c.mask.copy_(keep)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_interleaved_sequences(e4m3):
+    """Queries of one sequence not side by side: still right."""
+    c = Case(e4m3, 128, 2, 2, lens=(100, 64, 33), per=(4, 4, 4), seed=37)
+    order = [0, 4, 8, 1, 5, 9, 2, 6, 10, 3, 7, 11]
+    c.seq, c.pos = [c.seq[i] for i in order], [c.pos[i] - (i % 3) for i in order]
+    c.poison()
+    c.run()
+
+
+@pytest.mark.parametrize("k", [0, 40])
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_values_seen_by_some(e4m3, k):
+    """NaN and infinities in a drafted value or at a causal border reach the queries that see them, no others."""
+    c = Case(e4m3, 128, 2, 3, lens=(70, 90), per=(6, 6), k=k, drafts=6, seed=38)
+    bad = {0: int(c.start[0]) + 2, 1: 85}
+    c.pos[6:] = [80, 81, 84, 85, 86, 89]
+    if k:
+        c.topk[6:, 0] = 85                             # listed by all, in the prefix of three
+    for s, t in bad.items():
+        if e4m3:
+            c.v[s, t, 1, 5] = 0xFF
+            c.v[s, t, 0, 64] = 0x7F
+        else:
+            c.v[s, t, 1, 5] = math.nan
+            c.v[s, t, 0, 64] = -math.inf
+    out, lse = c.run(check=False)
+    hit = [i for i in range(c.n) if bad[c.seq[i]] in c.sees(i)]
+    assert 0 < len(hit) < c.n
+    o = out.double().view(c.n, 2, 3, 128)
+    for i in range(c.n):
+        where = ~torch.isfinite(o[i])
+        if i in hit:
+            assert bool(where[1, :, 5].all()) and bool(where[0, :, 64].all()) and int(where.sum()) == 6
+        else:
+            assert not bool(where.any())
+    c.check(out, lse, only=[i for i in range(c.n) if i not in hit])
+
+
+def test_a_nan_key_reaches_its_reader_only():
+    c = Case(False, 128, 1, 2, lens=(70,), per=(3,), drafts=3, seed=39)
+    c.mask.copy_(ints([[1], [3], [5]]))
+    c.k[0, int(c.start[0]) + 1, 0, 7] = math.nan
+    out, lse = c.run(check=False)
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(lse[1]).all())
+    c.check(out, lse, only=[0, 2])
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_large_and_negative_logits(e4m3):
+    for scale in (8.0, -0.3, 1e-6, 0.0):
+        c = Case(e4m3, 64, 2, 3, lens=(400, 90), per=(2, 2), seed=40, spread=0.2)
+        c.run(scale=scale)
+
+
+def test_scales_of_very_different_size():
+    """e4m3 rows whose scales span many orders, zero among them."""
+    c = Case(True, 128, 2, 4, lens=(500, 90), per=(2, 2), k=80, seed=41, spread=6.0)
+    c.ks.clamp_(max=0.02)
+    c.vs[:, ::7] = 0.0
+    c.run()
+    c.topk = None
+    c.run()
+
+
+def test_far_offsets():
+    """A cache beyond 2^32 bytes and 2^31 elements: rows of its far end."""
+    L, H_kv, d = 1 << 18, 80, 128
+    kv = A.KVCache.empty(2, L, H_kv, d, True)
+    assert kv.k.numel() > 1 << 32
+    g = gen(42)
+    k, v = (randn(g, 2, 50, H_kv, d).bfloat16() for _ in range(2))
+    pos = ints([L - 50, L - 50])
+    A.append_kv(kv, k, v, pos)
+    assert kv.device_status() == 0 and kv.seq_len.tolist() == [L, L]
+    ko, vo = A.read_kv(kv, ints([1]), ints([[L - 1, L - 50]]))
+    want, sc = plain_codes(k[1])
+    deq = (want.view(torch.float8_e4m3fn).float() * sc[..., None]).bfloat16()
+    assert torch.equal(ko[0], deq[[49, 0]])
+    c = Case.__new__(Case)
+    c.e4m3, c.d, c.H_kv, c.G, c.lens, c.draft, c.cap = True, d, H_kv, 1, (L, L), None, L
+    c.k, c.v, c.ks, c.vs, c.kv = kv.k, kv.v, kv.k_scale, kv.v_scale, kv
+    c.seq, c.pos, c.n = [1, 0], [L - 1, L - 3], 2
+    c.q = randn(g, 2, H_kv, d).bfloat16()
+    c.topk = torch.arange(L - 60, L, device=DEV).int().repeat(2, 1)
+    c.run()
+
+
+def test_streams_and_graphs():
+    c = Case(True, 128, 2, 4, lens=(5000, 777), per=(2, 1), k=300, drafts=2, seed=50)
+    ws = M.Workspace(DEV)
+    qs = c.queries()
+    want, wl = c.run(ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = A.attend(c.kv, qs, topk=c.topk, draft=c.draft, with_lse=True, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    # two graphs that share a workspace, replayed in turn on new inputs
+    p = Case(True, 128, 2, 4, lens=(5000, 777), per=(2, 1), seed=51)
+    pq, pw = p.queries(), p.run(ws=ws)
+    graphs = []
+    for case, q in ((c, qs), (p, pq)):
+        o, l_ = torch.empty_like(q.q), torch.empty(q.n_q, q.H, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            A.attend(case.kv, q, topk=case.topk, draft=case.draft, out=o, lse=l_, ws=ws)
+        graphs.append((g, o, l_))
+    ws.get(ws.buf.numel() * 4)                         # outgrown: the graphs' addresses stay good
+    for _ in range(3):
+        for g, o, l_ in graphs:
+            o.zero_(), l_.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1], want) and torch.equal(graphs[0][2], wl)
+    assert torch.equal(graphs[1][1], pw[0]) and torch.equal(graphs[1][2], pw[1])
+    c.q.copy_(c.q.flip(0))
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    c.check(graphs[0][1], graphs[0][2])
+
+
+def test_same_call_same_bits():
+    c = Case(False, 128, 4, 4, lens=(30000, 777), per=(3, 2), seed=52)
+    a = c.run()
+    for _ in range(3):
+        b = c.run(check=False)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_outputs_of_other_rows_stay():
+    c = Case(True, 128, 2, 4, lens=(300,), per=(2,), k=50, seed=53)
+    big = torch.full((6, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((6, 8), 3.0, device=DEV)
+    out, l_ = c.run(out=big[2:4], lse=lse[2:4])
+    assert bool((big[:2] == 3).all()) and bool((big[4:] == 3).all()) and bool((lse[:2] == 3).all()) and bool((lse[4:] == 3).all())
+
+
+def test_bits_and_bf16_tensors_are_the_same():
+    c = Case(False, 128, 2, 2, lens=(100,), per=(2,), seed=54)
+    want, wl = c.run()
+    kv = A.KVCache(c.k.view(torch.int16), c.v.view(torch.int16), None, None, ints(c.lens))
+    out, lse = A.attend(kv, A.AttentionQueries(c.q.view(torch.int16), ints(c.seq), ints(c.pos)), with_lse=True)
+    assert out.dtype == torch.int16 and torch.equal(out.view(torch.bfloat16), want) and torch.equal(lse, wl)
+
+
+def test_a_run_of_them_together():
+    """A prompt written, a decode step with selection, a drafted tree verified, its accepted path committed."""
+    g = gen(60)
+    n_seq, L0, H_kv, G, d, k = 2, 400, 2, 4, 128, 64
+    r = A.Rope(64, base=500000.0, layout="interleaved", scaling="yarn", factor=8.0)
+    kv = A.KVCache.empty(n_seq, 512, H_kv, d, True)
+    c = Case.__new__(Case)
+    c.e4m3, c.d, c.H_kv, c.G, c.cap, c.kv = True, d, H_kv, G, 512, kv
+    c.k, c.v, c.ks, c.vs, c.draft, c.topk = kv.k, kv.v, kv.k_scale, kv.v_scale, None, None
+    # prompt
+    new = [randn(g, n_seq, L0, H_kv, d).bfloat16() for _ in range(2)]
+    A.append_kv(kv, *new, ints([0, 0]), rope=r)
+    # one decode step: index keys and queries rotated, appended, selected by the dense indexer, attended
+    keys = torch.zeros(n_seq, 512, 128, dtype=torch.int16, device=DEV)
+    cache = M.KeyCache(keys, None, ints([L0, L0]), 64)
+    ik = randn(g, n_seq * L0, 1, 128).bfloat16()
+    pos_all = torch.arange(L0, device=DEV).int().repeat(n_seq)
+    A.apply_rope(r, [(ik, pos_all, ik)])
+    keys[:, :L0] = ik.view(torch.int16).view(n_seq, L0, 128)
+    M.pool_keys(cache)
+    iq, q = randn(g, n_seq, 16, 128).bfloat16(), randn(g, n_seq, H_kv * G, d).bfloat16()
+    pos = ints([L0, L0])
+    nk = randn(g, n_seq, 1, 128).bfloat16()
+    A.apply_rope(r, [(iq, pos, iq), (nk, pos, nk), (q, pos, q)])
+    M.pool_keys(cache, nk.view(torch.int16), None, pos)
+    A.append_kv(kv, randn(g, n_seq, 1, H_kv, d).bfloat16(), randn(g, n_seq, 1, H_kv, d).bfloat16(), pos, rope=r)
+    seq = ints([0, 1])
+    qs = M.Queries(iq.view(torch.int16), randn(g, n_seq, 16), seq, pos)
+    c.topk = M.dense_score_topk(cache, qs, k)
+    c.seq, c.pos, c.n, c.lens, c.q = [0, 1], [L0, L0], 2, (L0 + 1, L0 + 1), q
+    c.run()
+    assert kv.device_status() == 0 and cache.device_status() == 0
+    # five drafted tokens in a tree, at the positions of their depths
+    parents, T = [-1, 0, 0, 1, 2], 5
+    depth = ints([[0, 1, 1, 2, 2]] * n_seq) + L0 + 1
+    dk, dv = (randn(g, n_seq, T, H_kv, d).bfloat16() for _ in range(2))
+    start = ints([L0 + 1, L0 + 1])
+    A.append_kv(kv, dk, dv, start, rope=r, rope_pos=depth, commit=False)
+    assert kv.seq_len.tolist() == [L0 + 1] * 2
+    c.q = randn(g, n_seq * T, H_kv * G, d).bfloat16()
+    A.apply_rope(r, [(c.q, depth.view(-1), c.q)])
+    c.seq, c.pos, c.n = [0] * T + [1] * T, [L0] * (2 * T), 2 * T
+    c.mask, c.start, c.drafts = A.tree_mask(parents).repeat(n_seq, 1).to(DEV), start, T
+    c.draft = A.Draft(start, c.mask, T)
+    c.topk = c.topk.repeat_interleave(T, 0).contiguous()
+    tree_out, _ = c.run()
+    # accept nodes 0, 2, 4 of sequence 0, node 0 of sequence 1: written again at their places
+    for s, path in ((0, [0, 2, 4]), (1, [0])):
+        at = ints([L0 + 1 if x == s else -1 for x in range(n_seq)])
+        A.append_kv(kv, dk[:, path], dv[:, path], at, rope=r)
+    assert kv.seq_len.tolist() == [L0 + 4, L0 + 2]
+    # the accepted node's query, over the committed prefix: what the tree gave it
+    c.draft, c.topk = None, torch.cat([c.topk[[4, 5]], ints([[L0 + 1, L0 + 2, L0 + 3], [L0 + 1, -1, -1]])], dim=1)
+    c.lens, c.n, c.seq, c.pos, c.q = (L0 + 4, L0 + 2), 2, [0, 1], [L0 + 3, L0 + 1], c.q[[4, 5]].contiguous()
+    out, _ = c.run()
+    # the same tokens and bits in another order of sums: within both calls' bounds of one exact value
+    assert float((out.double() - tree_out[[4, 5]].double()).abs().max()) <= 4 * BF16 * float(out.abs().max())
+    assert kv.device_status() == 0
