@@ -5,28 +5,32 @@
 //   lse = ln sum_t e^(s_t)    over the tokens t that the query sees
 //
 // One pass over the tokens with a running maximum and sum per row (a row is a
-// head of a query).  The G = H / H_kv heads that read one key/value head are
-// the rows of a matrix tile, so a token's key and value are fetched once for
-// all of them: bound by the rows' bytes (e4m3, d = 128: 264 bytes per token
-// and key/value head against 4 G d flops) for the few rows of decode.
+// head of a query).  The G = H / H_kv heads that read one key/value head (and,
+// without lists, the neighbouring queries of one sequence) are the rows of a
+// tile, so a token's key and value are fetched once for all of them.
 //
-// attend_kernel: a CTA of 8 warps holds 16 MT rows of one key/value head and
-// a share of the tokens (blockIdx.z of Z shares).  Each warp runs alone
-// through every 8th chunk of CH tokens: it gathers the rows with 16-byte
-// cp.async into its own ring of STAGES chunks, so no barrier sits in the loop
-// and about 128 KB of rows are in flight per SM.  S = Q K^T and O += P V are
-// mma.sync m16n8k16 with fp32 sums.  The 8 warps' (max, sum, O) meet in shared
-// memory at the end; with Z > 1 the CTAs' meet in the workspace, where
-// attend_combine_kernel joins them in a fixed order.
+// attend_kernel: a CTA holds up to 8 NR rows of one key/value head and a share
+// of the tokens (blockIdx.z of Z shares).  Each warp runs alone through every
+// NW-th chunk of 16 tokens: it gathers the chunk's rows with 16-byte cp.async
+// into its own ring of three chunks, so no barrier sits in the loop and 100 to
+// 130 KB of rows are in flight per SM.  The tokens are the M side of mma.sync
+// m16n8k16 (S^T = K Q^T, O^T += V^T P^T), the rows the N side: 8 rows pad
+// nothing where M would pad to 16, and a lane keeps two tokens' scales.  P^T
+// turns from accumulator to operand by movmatrix.  The maximum is lazy: while
+// no logit exceeds the reference by 2^8 (base 2) nothing is rescaled and no
+// lane exchanges anything.
+// The warps' (max, sum, O) meet in shared memory at the end; with Z > 1 the
+// CTAs' meet in the workspace, where attend_combine_kernel joins them in a
+// fixed order.
 //
-// Numbers.  bf16 caches: bf16 products; the weights e^(s - max) are rounded to
+// Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
 // bf16 before they meet the values.  e4m3 caches: codes are exact in f16; a
 // query row is scaled by a power of two into f16's range (bf16 has 8
 // significant bits, so elements down to 2^-24 of the row's largest stay
-// exact); the weights of the sum are e^(s_t - max s) in fp32, and what meets
-// the value codes is e^(s_t - max s) v_scale_t 2^-c <= 1 in f16, with c the
-// running maximum of log2 of the contributions (relative to max s): so the
-// largest contribution of a row sets f16's range, not the largest scale.
+// exact); the weights of the sum are e^(s_t - ref) in fp32, and what meets the
+// value codes is e^(s_t - ref) v_scale_t 2^-c in f16, with c such that the
+// row's largest contribution lies in [2^-8, 2^8]: the largest contribution
+// sets f16's range, not the largest scale.
 #include <algorithm>
 
 #include "attention.h"
@@ -34,12 +38,13 @@
 namespace misa {
 namespace {
 
-constexpr int NW = 8;  // warps per CTA
-constexpr int THREADS = NW * 32;
+constexpr int CH = 16;  // tokens per chunk
 constexpr int STAGES = 3;
+constexpr float LAZY = 8.f;  // base-2 headroom of the running maximum
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr uint32_t ALL = (1u << CH) - 1u;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -52,6 +57,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+
+// 8 x 8 matrix of 16-bit values across the warp, transposed
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
@@ -71,20 +83,34 @@ __device__ __forceinline__ float row_scale(float amax) {
   return ldexpf(1.f, min(max(e, -126), 126));
 }
 
-template <int DH, bool FP8>
+__host__ __device__ constexpr int ctas_per_sm(bool fp8, int d, int nr) {
+  return fp8 ? (nr > 2 ? 1 : 2) : d > 64 ? 2 : nr > 2 ? 3 : 4;
+}
+
+template <int DH_, bool FP8_, int NR_>
 struct Cfg {
-  static constexpr int CH = FP8 ? 32 : 16;          // tokens per chunk
-  static constexpr int RB = DH * (FP8 ? 1 : 2);     // bytes per row
-  static constexpr int CPR = RB / 16;               // 16-byte pieces per row
-  static constexpr int KT = DH / 16;                // k-tiles of S
-  static constexpr int NT = CH / 8;                 // token n-tiles of S
-  static constexpr int VT = DH / 8;                 // value n-tiles of O
-  static constexpr int STAGE = 2 * CH * RB + (FP8 ? 2 * CH * 4 : 0) + 16;  // keys, values, scales, mask word
+  static constexpr int DH = DH_, NR = NR_;
+  static constexpr bool FP8 = FP8_;
+  static constexpr int RB = DH * (FP8 ? 1 : 2);  // bytes per row
+  static constexpr int CPR = RB / 16;            // 16-byte pieces per row
+  static constexpr int KT = DH / 16;             // k-tiles of S, m-tiles of O
+  static constexpr int STAGE = 2 * CH * RB + (FP8 ? 2 * CH * 4 : 0);  // keys, values, their scales
+  // Warps per CTA and CTAs per SM: 16 warps of an e4m3 kernel (whose codes
+  // are widened in registers) or 8 of a bf16 one fill the SM's shared memory
+  // with their rings; 32 rows take the registers of 8 warps.
+  static constexpr int NW = FP8 ? 8 : 4;
+  static constexpr int CTAS = ctas_per_sm(FP8, DH, NR);
+  static constexpr int THREADS = NW * 32;
+  static constexpr int R = 8 * NR;
+  static constexpr int OROW = DH + 8;  // floats between rows of a warp's result
+  static constexpr size_t RING = (size_t)NW * STAGES * STAGE;
+  static constexpr size_t JOIN = (size_t)NW * R * (OROW * 4 + 16);
+  static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
 };
 
 // Piece `c` of row `r`: keys are read as 16-byte pieces of two neighbouring
 // rows per quarter warp, values by ldmatrix over 8 rows; both without bank
-// conflicts under these permutations.
+// conflicts under these permutations (each its own inverse).
 template <int RB>
 __device__ __forceinline__ int k_piece(int r, int c) {
   return RB >= 128 ? c ^ ((r & 1) << 2) : c;
@@ -112,542 +138,577 @@ __device__ __forceinline__ int attend_prefix(const KvView &c, const AttendView &
   return p + 1;
 }
 
-// The queries of a CTA's rows that share a sequence, and the chunks of its
-// prefix and drafted tokens.
-struct Run {
-  int seq, len;      // longest prefix of its rows
-  int row0, row1;    // rows of the CTA
-  int c0, c1, c2;    // chunks [c0, c1): prefix, [c1, c2): drafted
-  int draft0;        // position of drafted slot 0
+// Queries [q0, q0 + n) of one sequence that a tile holds.
+struct Tile {
+  int q0, n;
 };
 
-template <int MT>
-struct RowInfo {
-  int len[16 * MT];    // prefix length (0 for rows that hold nothing)
-  int query[16 * MT];  // -1: no such row
-};
+// Tile number `want` of the batch without lists: runs of neighbouring queries
+// of one sequence (cut at multiples of 1024 queries) are dealt to tiles of up
+// to `per` queries, in order.  Every thread of the block calls; n == 0 when
+// there is no such tile.
+template <int THREADS>
+__device__ Tile find_tile(const AttendView &a, int per, int want) {
+  constexpr int SPAN = 1024, PER_T = SPAN / THREADS, NWARP = THREADS / 32;
+  __shared__ int seq_s[SPAN];
+  __shared__ int part[NWARP + 1];
+  __shared__ Tile found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) found = {0, 0};
+  for (int base = 0; base < a.n_q; base += SPAN) {
+    const int m = min(SPAN, a.n_q - base);
+    __syncthreads();
+    for (int i = tid; i < m; i += THREADS) seq_s[i] = a.q_seq[base + i];
+    __syncthreads();
+    // start of each query's run: a running maximum of the run starts
+    int start[PER_T], mx = 0;
+#pragma unroll
+    for (int e = 0; e < PER_T; ++e) {
+      const int i = tid * PER_T + e;
+      if (i < m && i > 0 && seq_s[i] != seq_s[i - 1]) mx = i;
+      start[e] = mx;
+    }
+    int incl = mx;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = max(incl, x);
+    }
+    int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0;
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before = max(before, part[w]);
+    // queries that lead a tile, counted in order
+    int lead = 0;
+    bool is[PER_T];
+#pragma unroll
+    for (int e = 0; e < PER_T; ++e) {
+      const int i = tid * PER_T + e;
+      is[e] = i < m && (i - max(start[e], before)) % per == 0;
+      lead += is[e];
+    }
+    int sum = lead;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = sum;
+    __syncthreads();
+    int first = sum - lead, total = 0;
+    for (int w = 0; w < NWARP; ++w) {
+      if (w < warp) first += part[w];
+      total += part[w];
+    }
+#pragma unroll
+    for (int e = 0; e < PER_T; ++e) {
+      if (!is[e]) continue;
+      if (first++ == want) {
+        const int i = tid * PER_T + e;
+        int n = 1;
+        while (n < per && i + n < m && seq_s[i + n] == seq_s[i]) ++n;
+        found = {base + i, n};
+      }
+    }
+    if (want < total) break;
+    want -= total;
+  }
+  __syncthreads();
+  const Tile t = found;
+  __syncthreads();
+  return t;
+}
 
 struct Split {
-  float *o;      // [Z][n_q * H][DH]
-  float4 *ml;    // [Z][n_q * H] (max, sum, reference of O)
+  float *o;    // [Z][n_q * H][DH]
+  float4 *ml;  // [Z][n_q * H] (max, sum, reference of O)
   int Z;
 };
 
-template <int DH, bool FP8, int MT, bool LIST>
-__global__ void __launch_bounds__(THREADS, 1)
-    attend_kernel(KvView c, AttendView a, Split split, int tiles_per_query) {
+// LIST: blockIdx.x = query * row_tiles + tile of its G heads.  Otherwise
+// blockIdx.x = tile of `per` queries * row_tiles + tile of their rows, with
+// row_tiles > 1 only for per == 1.
+template <class F, bool LIST>
+__global__ void __launch_bounds__(F::THREADS, F::CTAS)
+    attend_kernel(KvView c, AttendView a, Split split, int per, int row_tiles) {
   grid_dep_sync();
-  using F = Cfg<DH, FP8>;
-  constexpr int R = 16 * MT, CH = F::CH, RB = F::RB;
+  constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT, NW = F::NW;
+  constexpr bool FP8 = F::FP8;
+  constexpr bool Q_SMEM = NR > (FP8 ? 1 : 2);  // the query fragments do not fit beside O
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ RowInfo<MT> rows;
-  __shared__ Run runs[R];
-  __shared__ int n_runs_s;
-  __shared__ __align__(16) uint4 qfrag[MT * F::KT * 32];
-  __shared__ float row_mul[R];  // scale log2(e) over the row's power of two
+  __shared__ uint2 q_s[Q_SMEM ? KT * NR * 32 : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
   const int G = a.H / c.H_kv, hk = blockIdx.y, Z = split.Z;
-  const int tile = blockIdx.x;
-  // row r of the CTA -> query and head
-  const int q0 = LIST ? tile / tiles_per_query : 0;
-  const int g0 = LIST ? (tile % tiles_per_query) * R : 0;
-  auto row_query = [&](int r) -> int {
-    if (LIST) return g0 + r < G ? q0 : -1;
-    const int64_t x = (int64_t)tile * R + r;
-    return x < (int64_t)a.n_q * G ? (int)(x / G) : -1;
-  };
-  auto row_head = [&](int r) -> int {
-    return hk * G + (LIST ? g0 + r : (int)(((int64_t)tile * R + r) % G));
-  };
+  const int row_tile = blockIdx.x % row_tiles, g0 = row_tile * R;
+  int tile_i = blockIdx.x / row_tiles;
+  const int tile_step = gridDim.x / row_tiles;
+  Tile t = {tile_i, 1};
+  if (!LIST) t = find_tile<F::THREADS>(a, per, tile_i);
 
-  // ---- rows, runs ----
-  __shared__ int row_seq[R];
-  if (tid < R) {
-    const int q = row_query(tid);
-    int s = -1, len = 0;
-    if (q >= 0) len = attend_prefix(c, a, q, &s);
-    rows.query[tid] = q;
-    rows.len[tid] = len;
-    row_seq[tid] = s;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int n = 0, chunks = 0;
-    for (int r = 0; r < R;) {
-      if (row_seq[r] < 0) {
-        ++r;
-        continue;
-      }
-      Run u;
-      u.seq = row_seq[r];
-      u.row0 = r;
-      u.len = 0;
-      while (r < R && row_seq[r] == u.seq) u.len = max(u.len, rows.len[r++]);
-      u.row1 = r;
-      u.c0 = chunks;
-      chunks += LIST ? cdiv(a.k, CH) : cdiv(u.len, CH);
-      u.c1 = chunks;
-      u.draft0 = 0;
-      if (a.draft_start) {
-        chunks += cdiv(a.n_draft, CH);
-        u.draft0 = a.draft_start[u.seq];
-      }
-      u.c2 = chunks;
-      runs[n++] = u;
-    }
-    n_runs_s = n;
-  }
-  // ---- query fragments: the k dimension permuted so that a 16-byte piece of
-  // a key row feeds whole B fragments (see tile loop) ----
-  for (int r = warp; r < R; r += NW) {
-    const int q = row_query(r);
-    float sc = 1.f;
-    if (FP8) {
-      float m = 0.f;
-      if (q >= 0) {
-        const uint16_t *src = a.q + ((int64_t)q * a.H + row_head(r)) * DH;
-        for (int e = lane; e < DH; e += 32) {
-          const float x = fabsf(bf16_bits_to_float(src[e]));
-          m = (x > m || x != x) ? x : m;  // a NaN stays
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, m, o);
-        m = (x > m || x != x) ? x : m;
-      }
-      sc = row_scale(m);
-    }
-    if (lane == 0) row_mul[r] = sc;
-  }
-  __syncthreads();
-  for (int e = tid; e < MT * F::KT * 32; e += THREADS) {
-    const int l = e & 31, kt = (e >> 5) % F::KT, mt = (e >> 5) / F::KT;
-    // FP8: piece of 16 elements feeds 4 k-tiles; bf16: of 8 elements, 2
-    const int ch = FP8 ? kt >> 2 : kt >> 1, u = FP8 ? kt & 3 : kt & 1;
-    const int d0 = FP8 ? 64 * ch + 16 * (l & 3) + 4 * u : 32 * ch + 8 * (l & 3) + 4 * u;
-    uint32_t w[4];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = mt * 16 + (l >> 2) + 8 * half;
-      const int q = row_query(r);
-      uint2 v = make_uint2(0u, 0u);
-      if (q >= 0) v = *reinterpret_cast<const uint2 *>(a.q + ((int64_t)q * a.H + row_head(r)) * DH + d0);
-      if (FP8) {
-        const float sc = row_mul[r];
-        const float2 x = bf16x2_to_float2(v.x), y = bf16x2_to_float2(v.y);
-        v.x = f16x2(x.x * sc, x.y * sc);
-        v.y = f16x2(y.x * sc, y.y * sc);
-      }
-      w[half] = v.x;
-      w[2 + half] = v.y;
-    }
-    qfrag[e] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __syncthreads();
-  if (tid < R) row_mul[tid] = a.scale * LOG2E / row_mul[tid];
-  __syncthreads();
+  for (; t.n > 0;) {
+    const int n_rows = per > 1 ? t.n * G : min(G - g0, R);
+    auto row_query = [&](int r) { return per > 1 ? t.q0 + r / G : t.q0; };
+    auto row_head = [&](int r) { return hk * G + (per > 1 ? r % G : g0 + r); };
 
-  // ---- this CTA's chunks, every NW-th to a warp ----
-  const int n_runs = n_runs_s;
-  const int chunks = n_runs ? runs[n_runs - 1].c2 : 0;
-  const int share = cdiv(chunks, Z);
-  const int cb = min((int)blockIdx.z * share, chunks), ce = min(cb + share, chunks);
-
-  float o[MT][F::VT][4];
-  // base 2: running maximum of the logits, sum of the weights relative to it,
-  // and the exponent that O is relative to (bf16 caches: the maximum itself)
-  float m_run[MT][2], l_run[MT][2], y_run[MT][2];
+    // ---- the tile's tokens: prefix (or list) chunks, then drafted chunks ----
+    int seq, len = 0;
+    int col_len[NR][2];  // this lane's two columns (rows of the tile) of each n-tile
+    if (LIST) {
+      len = attend_prefix(c, a, t.q0, &seq);
+    } else {
+      seq = -1;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int n = 0; n < F::VT; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
-    m_run[mt][0] = m_run[mt][1] = y_run[mt][0] = y_run[mt][1] = NEG_INF;
-    l_run[mt][0] = l_run[mt][1] = 0.f;
-  }
-
-  uint8_t *ring = smem + warp * (STAGES * F::STAGE);
-  auto stage_k = [&](int st) { return ring + st * F::STAGE; };
-  auto stage_v = [&](int st) { return ring + st * F::STAGE + CH * RB; };
-  auto stage_s = [&](int st) { return reinterpret_cast<float *>(ring + st * F::STAGE + 2 * CH * RB); };
-  auto stage_m = [&](int st) {
-    return reinterpret_cast<uint32_t *>(ring + st * F::STAGE + F::STAGE - 16);
-  };
-
-  // Position of this lane's token of a chunk (lane < CH), -1 for none.
-  int run_i = 0;  // run of the chunk last asked for (chunks ascend)
-  auto token_of = [&](int ck) -> int {
-    if (ck >= ce) return -1;
-    while (ck >= runs[run_i].c2) ++run_i;
-    const Run &u = runs[run_i];
-    const int l = lane & (CH - 1);
-    if (ck >= u.c1) {
-      const int j = (ck - u.c1) * CH + l;
-      if (j >= a.n_draft) return -1;
-      bool want = true;
-      if (LIST) want = (a.draft_mask[(int64_t)q0 * cdiv(a.n_draft, 32) + (j >> 5)] >> (j & 31)) & 1u;
-      if (!want) return -1;
-      const int64_t p = (int64_t)u.draft0 + j;
-      if (p >= 0 && p < c.L_cap) return (int)p;
-      if (LIST) flag(c, MISA_DEV_BAD_POSITION);
-      return -1;
-    }
-    const int t = (ck - u.c0) * CH + l;
-    if (!LIST) return t < u.len ? t : -1;
-    if (t >= a.k) return -1;
-    const int tok = __ldg(a.topk + (int64_t)q0 * a.k + t);
-    return tok >= 0 && tok < u.len ? tok : -1;
-  };
-  // Gather chunk rows into stage st.
-  auto issue = [&](int st, int ck, int tok) {
-    if (ck < ce) {
-      const uint32_t have = __ballot_sync(0xffffffffu, tok >= 0);
-      const int64_t base = (int64_t)runs[run_i].seq * c.L_cap;
-      if (have) {
-        const uint32_t sk = smem_addr(stage_k(st)), sv = smem_addr(stage_v(st));
-#pragma unroll
-        for (int it = 0; it < CH * F::CPR / 32; ++it) {
-          const int r = it * (32 / F::CPR) + lane / F::CPR, pc = lane % F::CPR;
-          const int t = __shfl_sync(0xffffffffu, tok, r);
-          const int64_t off = ((base + max(t, 0)) * c.H_kv + hk) * RB + pc * 16;
-          cp_async16(sk + r * RB + k_piece<RB>(r, pc) * 16, c.k + off, t >= 0);
-          cp_async16(sv + r * RB + v_piece<RB>(r, pc) * 16, c.v + off, t >= 0);
-        }
-        if (FP8 && lane < CH) {
-          const int64_t row = (base + max(tok, 0)) * c.H_kv + hk;
-          const uint32_t ss = smem_addr(stage_s(st));
-          cp_async4(ss + lane * 4, c.k_scale + row, tok >= 0);
-          cp_async4(ss + (CH + lane) * 4, c.v_scale + row, tok >= 0);
-        }
-      }
-      if (lane == 0) *stage_m(st) = CH == 32 ? have : have & 0xFFFFu;
-    }
-    cp_async_commit();
-  };
-
-  int nxt = cb + warp;  // next chunk to issue
-  int tok_n = token_of(nxt);
-#pragma unroll
-  for (int st = 0; st < STAGES - 1; ++st) {
-    issue(st, nxt, tok_n);
-    nxt += NW;
-    tok_n = token_of(nxt);
-  }
-  int st = 0, run_c = 0;
-  for (int ck = cb + warp; ck < ce; ck += NW) {
-    cp_async_wait<STAGES - 2>();
-    __syncwarp();
-    const int wr = st == 0 ? STAGES - 1 : st - 1;
-    const uint32_t have = *stage_m(st);
-    // (the stage written now was last read in the iteration before; the
-    // __syncwarp above orders those reads)
-    issue(wr, nxt, tok_n);
-    nxt += NW;
-    tok_n = token_of(nxt);
-    const uint8_t *sk = stage_k(st), *sv = stage_v(st);
-    const float *ss = stage_s(st);
-    st = st == STAGES - 1 ? 0 : st + 1;
-    if (!have) continue;
-    while (ck >= runs[run_c].c2) ++run_c;
-    const Run &u = runs[run_c];
-
-    // ---- S = Q K^T ----
-    float s[MT][F::NT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int n = 0; n < F::NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
-#pragma unroll
-    for (int ch = 0; ch < RB / 64; ++ch) {
-      uint4 kv[F::NT];
-#pragma unroll
-      for (int n = 0; n < F::NT; ++n) {
-        const int r = n * 8 + g;
-        kv[n] = *reinterpret_cast<const uint4 *>(sk + r * RB + k_piece<RB>(r, 4 * ch + c4) * 16);
-      }
-#pragma unroll
-      for (int uu = 0; uu < (FP8 ? 4 : 2); ++uu) {
-        const int kt = ch * (FP8 ? 4 : 2) + uu;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint4 qf = qfrag[(mt * F::KT + kt) * 32 + lane];
-          const uint32_t af[4] = {qf.x, qf.y, qf.z, qf.w};
-#pragma unroll
-          for (int n = 0; n < F::NT; ++n) {
-            if (FP8) {
-              const uint32_t w = uu == 0 ? kv[n].x : uu == 1 ? kv[n].y : uu == 2 ? kv[n].z : kv[n].w;
-              mma_f16_16816(s[mt][n], af, e4m3x2_to_f16x2((uint16_t)w), e4m3x2_to_f16x2((uint16_t)(w >> 16)));
-            } else {
-              mma_bf16_16816(s[mt][n], af, uu ? kv[n].z : kv[n].x, uu ? kv[n].w : kv[n].y);
-            }
-          }
-        }
-      }
-    }
-
-    // ---- visible tokens, scales, running maximum ----
-    float lv[F::NT][2], vs[F::NT][2], ks[F::NT][2];
-    if (FP8) {
-#pragma unroll
-      for (int n = 0; n < F::NT; ++n) {
-        const float2 kk = *reinterpret_cast<const float2 *>(ss + n * 8 + 2 * c4);
-        const float2 vv = *reinterpret_cast<const float2 *>(ss + CH + n * 8 + 2 * c4);
-        ks[n][0] = kk.x, ks[n][1] = kk.y;
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          vs[n][x] = x ? vv.y : vv.x;
-          lv[n][x] = __log2f(vs[n][x] < 0x1p-100f ? 0x1p-100f : vs[n][x]);  // a NaN stays
+          const int r = n * 8 + 2 * c4 + x;
+          col_len[n][x] = -1;
+          if (r < n_rows) {
+            int s;
+            col_len[n][x] = attend_prefix(c, a, row_query(r), &s);
+            seq = max(seq, s);
+            len = max(len, col_len[n][x]);
+            if (s < 0) col_len[n][x] = -1;
+          }
         }
+      len = max(len, __shfl_xor_sync(0xffffffffu, len, 1));
+      len = max(len, __shfl_xor_sync(0xffffffffu, len, 2));
+      seq = max(seq, __shfl_xor_sync(0xffffffffu, seq, 1));
+      seq = max(seq, __shfl_xor_sync(0xffffffffu, seq, 2));
+    }
+    const int c1 = seq < 0 ? 0 : cdiv(LIST ? a.k : len, CH);
+    const int chunks = c1 + (seq >= 0 && a.draft_start ? cdiv(a.n_draft, CH) : 0);
+    const int draft0 = seq >= 0 && a.draft_start ? a.draft_start[seq] : 0;
+    const int words = cdiv(a.n_draft, 32);
+    const int share = cdiv(chunks, Z);
+    const int cb = min((int)blockIdx.z * share, chunks), ce = min(cb + share, chunks);
+
+    // ---- query fragments, the k dimension permuted so that a lane's 16-byte
+    // pieces of a key row feed whole A fragments ----
+    uint2 qf[Q_SMEM ? 1 : KT][Q_SMEM ? 1 : NR];
+    float mul[NR][2];  // scale log2(e), over the row's power of two
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      if (Q_SMEM && n % NW != warp % NR) continue;  // warps beyond NR repeat, harmlessly
+      const int r = n * 8 + g;
+      const bool live = r < n_rows;
+      const uint16_t *src = a.q + ((int64_t)row_query(live ? r : 0) * a.H + row_head(live ? r : 0)) * DH;
+      uint4 raw[DH / 32];
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        // FP8: 16 elements at 64 ch + 16 c4 (pieces 2 ch, 2 ch + 1 of the
+        // lane); bf16: 8 at 32 i + 8 c4
+        const int d0 = FP8 ? 64 * (i >> 1) + 16 * c4 + 8 * (i & 1) : 32 * i + 8 * c4;
+        raw[i] = live ? *reinterpret_cast<const uint4 *>(src + d0) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float sc = 1.f;
+      if (FP8) {
+        float m = 0.f;
+        auto take = [&](float x) { m = (x > m || x != x) ? x : m; };  // a NaN stays
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float2 f = bf16x2_to_float2(w[p]);
+            take(fabsf(f.x));
+            take(fabsf(f.y));
+          }
+        }
+        take(__shfl_xor_sync(0xffffffffu, m, 1));
+        take(__shfl_xor_sync(0xffffffffu, m, 2));
+        sc = row_scale(m);
+      }
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        if (FP8) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float2 f = bf16x2_to_float2(w[p]);
+            w[p] = f16x2(f.x * sc, f.y * sc);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint2 v = make_uint2(w[2 * u], w[2 * u + 1]);
+          if (Q_SMEM)
+            q_s[((2 * i + u) * NR + n) * 32 + lane] = v;
+          else
+            qf[2 * i + u][n] = v;
+        }
+      }
+      // the multiplier of the lane's columns sits with the lanes of those rows
+      if (!Q_SMEM) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          mul[n][x] = a.scale * LOG2E / __shfl_sync(0xffffffffu, sc, (2 * c4 + x) * 4);
+      } else if (c4 == 0) {
+        reinterpret_cast<float *>(smem)[r] = sc;  // read before the rings are filled
       }
     }
-    uint32_t vis[MT][2];
-    bool mixed = false;  // some row does not see a gathered token
+    if (Q_SMEM) {
+      __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mt * 16 + g + 8 * hf;
+        for (int x = 0; x < 2; ++x) mul[n][x] = a.scale * LOG2E / reinterpret_cast<float *>(smem)[n * 8 + 2 * c4 + x];
+      __syncthreads();
+    }
+
+    float o[KT][NR][4];
+    // base 2, per column: reference of the weights' sum and the sum (this
+    // lane's tokens), reference of O (bf16 caches: the same) and the factor
+    // between the two
+    float m_ref[NR][2], l_sum[NR][2], y_ref[NR][2], fac[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m_ref[n][x] = y_ref[n][x] = NEG_INF;
+        l_sum[n][x] = 0.f;
+        fac[n][x] = 1.f;
+      }
+    }
+
+    uint8_t *ring = smem + warp * (STAGES * F::STAGE);
+    const uint32_t ring_a = smem_addr(ring);
+    const uint8_t *kb = c.k + (int64_t)max(seq, 0) * c.L_cap * c.H_kv * RB;
+    const uint8_t *vb = c.v + (int64_t)max(seq, 0) * c.L_cap * c.H_kv * RB;
+    const int64_t sb = (int64_t)max(seq, 0) * c.L_cap * c.H_kv;
+
+    // Row of this lane's token (lane & 15) of a chunk within its sequence's
+    // keys, token * H_kv + head (below 2^25); -1 for none.
+    auto row_of = [&](int ck) -> int {
+      if (ck >= ce) return -1;
+      const int l = lane & (CH - 1);
+      int tok;
+      if (ck < c1) {
+        const int i = ck * CH + l;
         if (LIST) {
-          vis[mt][hf] = rows.query[r] >= 0 ? have : 0u;
+          if (i >= a.k) return -1;
+          tok = __ldg(a.topk + (int64_t)t.q0 * a.k + i);
         } else {
-          uint32_t v = 0u;
-          if (r >= u.row0 && r < u.row1) {
-            if (ck < u.c1) {
-              const int nn = rows.len[r] - (ck - u.c0) * CH;
-              v = nn >= 32 ? 0xffffffffu : nn > 0 ? (1u << nn) - 1u : 0u;
-            } else {
-              const int j0 = (ck - u.c1) * CH;
-              v = a.draft_mask[(int64_t)rows.query[r] * cdiv(a.n_draft, 32) + (j0 >> 5)] >> (j0 & 31);
-              if (CH < 32) v &= (1u << CH) - 1u;
-              if ((a.n_draft - j0) < CH) v &= (1u << (a.n_draft - j0)) - 1u;
-              if ((v & ~have) && c4 == 0) flag(c, MISA_DEV_BAD_POSITION);
-            }
+          tok = i;
+        }
+        if (tok < 0 || tok >= len) return -1;
+      } else {
+        const int j = (ck - c1) * CH + l;
+        if (j >= a.n_draft) return -1;
+        if (LIST && !((a.draft_mask[(int64_t)t.q0 * words + (j >> 5)] >> (j & 31)) & 1u)) return -1;
+        const int64_t p = (int64_t)draft0 + j;
+        if (p < 0 || p >= c.L_cap) {
+          if (LIST) flag(c, MISA_DEV_BAD_POSITION);
+          return -1;
+        }
+        tok = (int)p;
+      }
+      return tok * c.H_kv + hk;
+    };
+    // Gather a chunk's rows into stage st; returns which tokens are there.
+    auto issue = [&](int st, int row) -> uint32_t {
+      const uint32_t have = __ballot_sync(0xffffffffu, row >= 0) & ALL;
+      if (have) {
+        const uint32_t sk = ring_a + st * F::STAGE, sv = sk + CH * RB;
+#pragma unroll
+        for (int it = 0; it < CH * CPR / 32; ++it) {
+          const int r = it * (32 / CPR) + lane / CPR, pc = lane % CPR;
+          const int x = __shfl_sync(0xffffffffu, row, r);
+          const int64_t off = (int64_t)(max(x, 0) * CPR + pc) * 16;  // below 2^29 pieces
+          cp_async16(sk + r * RB + k_piece<RB>(r, pc) * 16, kb + off, x >= 0);
+          cp_async16(sv + r * RB + v_piece<RB>(r, pc) * 16, vb + off, x >= 0);
+        }
+        if (FP8) cp_async4(sv + CH * RB + lane * 4, (lane < CH ? c.k_scale : c.v_scale) + sb + max(row, 0), row >= 0);
+      }
+      cp_async_commit();
+      return have;
+    };
+
+    int nxt = cb + warp;
+    int row_n = row_of(nxt);
+    uint32_t have_q[STAGES];
+#pragma unroll
+    for (int st = 0; st < STAGES - 1; ++st) {
+      have_q[st] = issue(st, row_n);
+      nxt += NW;
+      row_n = row_of(nxt);
+    }
+    int st = 0;
+    for (int ck = cb + warp; ck < ce; ck += NW) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies have landed, and its reads of the stage issued next are done
+      const uint32_t have = have_q[0];
+      have_q[0] = have_q[1];
+      have_q[1] = issue(st == 0 ? STAGES - 1 : st - 1, row_n);
+      nxt += NW;
+      row_n = row_of(nxt);
+      uint8_t *sk = ring + st * F::STAGE, *sv = sk + CH * RB;
+      const float *ss = reinterpret_cast<const float *>(sv + CH * RB);
+      st = st == STAGES - 1 ? 0 : st + 1;
+      if (!have) continue;
+
+      // ---- S^T = K Q^T ----
+      float s[NR][4];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+      for (int ch = 0; ch < RB / 64; ++ch) {
+        const uint4 A = *reinterpret_cast<const uint4 *>(sk + g * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
+        const uint4 B = *reinterpret_cast<const uint4 *>(sk + (g + 8) * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
+        const uint32_t wa[4] = {A.x, A.y, A.z, A.w}, wb[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+        for (int u = 0; u < (FP8 ? 4 : 2); ++u) {
+          const int kt = ch * (FP8 ? 4 : 2) + u;
+          uint32_t af[4];
+          if (FP8) {
+            af[0] = e4m3x2_to_f16x2((uint16_t)wa[u]), af[1] = e4m3x2_to_f16x2((uint16_t)wb[u]);
+            af[2] = e4m3x2_to_f16x2((uint16_t)(wa[u] >> 16)), af[3] = e4m3x2_to_f16x2((uint16_t)(wb[u] >> 16));
+          } else {
+            af[0] = wa[2 * u], af[1] = wb[2 * u], af[2] = wa[2 * u + 1], af[3] = wb[2 * u + 1];
           }
-          vis[mt][hf] = v & have;
-          mixed |= vis[mt][hf] != have;
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const uint2 q = Q_SMEM ? q_s[(kt * NR + n) * 32 + lane] : qf[Q_SMEM ? 0 : kt][Q_SMEM ? 0 : n];
+            if (FP8)
+              mma_f16_16816(s[n], af, q.x, q.y);
+            else
+              mma_bf16_16816(s[n], af, q.x, q.y);
+          }
         }
       }
+
+      // ---- base-2 logits of the tokens g and g + 8 (index y), columns x;
+      // what is not seen becomes -inf ----
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+      if (FP8) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+        for (int y = 0; y < 2; ++y) {
+          ks[y] = ss[g + 8 * y];
+          vs[y] = ss[CH + g + 8 * y];
+          lv[y] = __log2f(vs[y] < 0x1p-100f ? 0x1p-100f : vs[y]);  // a NaN stays
+        }
+      }
+      uint32_t vis[NR][2];
+      bool mixed = false;  // some row does not see a gathered token
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float mul = row_mul[mt * 16 + g + 8 * hf];
-        float mx = NEG_INF, my = NEG_INF;
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int n = 0; n < F::NT; ++n)
+        for (int x = 0; x < 2; ++x) {
+          uint32_t v = have;
+          if (!LIST) {
+            const int r = n * 8 + 2 * c4 + x;
+            if (col_len[n][x] < 0) {
+              v = 0u;
+            } else if (ck < c1) {
+              const int nn = col_len[n][x] - ck * CH;
+              v &= nn >= CH ? ALL : nn > 0 ? (1u << nn) - 1u : 0u;
+            } else {
+              const int j0 = (ck - c1) * CH;
+              uint32_t m = a.draft_mask[(int64_t)row_query(r) * words + (j0 >> 5)] >> (j0 & 31) & ALL;
+              if (a.n_draft - j0 < CH) m &= (1u << (a.n_draft - j0)) - 1u;
+              if (m & ~have) flag(c, MISA_DEV_BAD_POSITION);
+              v &= m;
+            }
+            mixed |= col_len[n][x] >= 0 && v != have;
+          }
+          vis[n][x] = v;
+        }
+      bool above = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float &v = s[n][2 * y + x];
+            v *= FP8 ? ks[y] * mul[n][x] : mul[n][x];
+            if ((!LIST || have != ALL) && !((vis[n][x] >> (g + 8 * y)) & 1u)) v = NEG_INF;
+            above |= v > m_ref[n][x] + LAZY;
+            if (FP8) above |= v + lv[y] > y_ref[n][x] + LAZY;
+          }
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float &v = s[mt][n][2 * hf + x];
-            v = FP8 ? v * ks[n][x] * mul : v * mul;
-            if (!((vis[mt][hf] >> (n * 8 + 2 * c4 + x)) & 1u)) v = NEG_INF;
-            mx = fmaxf(mx, v);
-            if (FP8) my = fmaxf(my, v + lv[n][x]);
+            float mx = fmaxf(s[n][x], s[n][2 + x]), my = fmaxf(s[n][x] + lv[0], s[n][2 + x] + lv[1]);
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
+              if (FP8) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));
+            }
+            if (!FP8) my = mx;
+            const float m_new = fmaxf(m_ref[n][x], mx), y_new = fmaxf(y_ref[n][x], my);
+            // a column without a visible token yet keeps -inf: its sums are 0
+            l_sum[n][x] *= m_new == NEG_INF ? 1.f : ex2(m_ref[n][x] - m_new);
+            const float al = y_new == NEG_INF ? 1.f : ex2(y_ref[n][x] - y_new);
+#pragma unroll
+            for (int j = 0; j < KT; ++j) o[j][n][x] *= al, o[j][n][2 + x] *= al;
+            m_ref[n][x] = m_new;
+            y_ref[n][x] = y_new;
+            fac[n][x] = m_new == NEG_INF || !FP8 ? 1.f : ex2(m_new - y_new);
           }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (FP8) {
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
-        } else {
-          my = mx;
-        }
-        const float m_new = fmaxf(m_run[mt][hf], mx), y_new = fmaxf(y_run[mt][hf], my);
-        const float ref = m_new == NEG_INF ? 0.f : m_new, yref = y_new == NEG_INF ? 0.f : y_new;
-        if (m_new != m_run[mt][hf]) {
-          l_run[mt][hf] *= ex2(m_run[mt][hf] - ref);
-          m_run[mt][hf] = m_new;
-        }
-        if (y_new != y_run[mt][hf]) {
-          const float al = ex2(y_run[mt][hf] - yref);
+      }
+      uint32_t pb[NR][2];
 #pragma unroll
-          for (int n = 0; n < F::VT; ++n) {
-            o[mt][n][2 * hf] *= al;
-            o[mt][n][2 * hf + 1] *= al;
-          }
-          y_run[mt][hf] = y_new;
-        }
-        const float f = FP8 ? ex2(ref - yref) : 1.f;
-        float sum = 0.f;
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int n = 0; n < F::NT; ++n)
+        for (int x = 0; x < 2; ++x) {
+          const float ref = m_ref[n][x] == NEG_INF ? 0.f : m_ref[n][x];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float &v = s[mt][n][2 * hf + x];
+          for (int y = 0; y < 2; ++y) {
+            float &v = s[n][2 * y + x];
+            // (rows gathered for others may hold any scale)
             const bool seen = LIST || v != NEG_INF;
             v = ex2(v - ref);
-            sum += v;
-            // (gathered rows that this one does not see may hold any scale)
-            if (FP8) v = seen ? v * (vs[n][x] * f) : 0.f;
+            l_sum[n][x] += v;
+            if (FP8) v = seen ? v * (vs[y] * fac[n][x]) : 0.f;
           }
-        l_run[mt][hf] += sum;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          pb[n][y] = movmatrix_trans(FP8 ? f16x2(s[n][2 * y], s[n][2 * y + 1]) : bf16x2(s[n][2 * y], s[n][2 * y + 1]));
       }
 
-    // ---- values that some rows must not see: a NaN or infinity there would
-    // reach them as 0 * NaN.  Such values are taken out of the tile and added
-    // to the rows that do see them ----
-    if (!LIST && __any_sync(0xffffffffu, mixed)) {
-      for (int e = lane; e < CH * RB / 4; e += 32) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(sv)[e];
-        bool bad;
-        if (FP8)
-          bad = (__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0u;
-        else
-          bad = (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-        uint32_t who = __ballot_sync(0xffffffffu, bad);
-        while (who) {
-          const int src = __ffs(who) - 1;
-          who &= who - 1;
-          const int be = e - lane + src;  // word of the tile
-          const uint32_t bw = __shfl_sync(0xffffffffu, w, src);
-          const int r = be / (RB / 4), off = (be % (RB / 4)) * 4;
-          const int pc = v_piece<RB>(r, off >> 4);  // the permutation is its own inverse
-          for (int b = 0; b < (FP8 ? 4 : 2); ++b) {
-            const uint32_t el = FP8 ? (bw >> (8 * b)) & 0xffu : (bw >> (16 * b)) & 0xffffu;
-            if (FP8 ? (el & 0x7fu) != 0x7fu : (el & 0x7f80u) != 0x7f80u) continue;
-            const float val = FP8 ? __int_as_float(0x7fffffff) : bf16_bits_to_float(el);
-            const int dd = FP8 ? pc * 16 + (off & 15) + b : (pc * 16 + (off & 15)) / 2 + b;
-            // accumulator of element dd: n-tile and register of its lane
-            const int n_of = FP8 ? 2 * (dd >> 4) + (dd & 1) : dd >> 3;
-            const int col = FP8 ? (dd & 15) >> 1 : dd & 7;  // column of the n-tile
+      // ---- values that some rows must not see: a NaN or infinity there would
+      // reach them as 0 * NaN.  Such values are taken out of the chunk and
+      // added to the rows that do see them ----
+      if (!LIST && __any_sync(0xffffffffu, mixed)) {
+        for (int e = lane; e < CH * RB / 4; e += 32) {
+          uint32_t *word = reinterpret_cast<uint32_t *>(sv) + e;
+          const uint32_t w = *word;
+          const bool bad = FP8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u
+                               : (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+          uint32_t who = __ballot_sync(0xffffffffu, bad);
+          while (who) {
+            const int src = __ffs(who) - 1;
+            who &= who - 1;
+            const uint32_t bw = __shfl_sync(0xffffffffu, w, src);
+            const int at = (e - lane + src) * 4, r = at / RB, off = at % RB;
+            const int d0 = (v_piece<RB>(r, off >> 4) * 16 + (off & 15)) / (FP8 ? 1 : 2);
+            for (int b = 0; b < (FP8 ? 4 : 2); ++b) {
+              const uint32_t el = FP8 ? (bw >> (8 * b)) & 0xffu : (bw >> (16 * b)) & 0xffffu;
+              if (FP8 ? (el & 0x7fu) != 0x7fu : (el & 0x7f80u) != 0x7f80u) continue;
+              const float val = FP8 ? __int_as_float(0x7fffffff) : bf16_bits_to_float(el);
+              const int jt = (d0 + b) >> 4, dd = (d0 + b) & 15;
+              const int gt = FP8 ? dd >> 1 : dd & 7, hi = FP8 ? dd & 1 : dd >> 3;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+              for (int n = 0; n < NR; ++n)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                float wt = 0.f;
+                for (int x = 0; x < 2; ++x) {
+                  const float wt = __shfl_sync(0xffffffffu, r < 8 ? s[n][x] : s[n][2 + x], (r & 7) * 4 + c4);
+                  if (g != gt || !((vis[n][x] >> r) & 1u)) continue;
 #pragma unroll
-                for (int n = 0; n < F::NT; ++n)
-#pragma unroll
-                  for (int x = 0; x < 2; ++x)
-                    if (n == (r >> 3) && x == (r & 1)) wt = s[mt][n][2 * hf + x];
-                wt = __shfl_sync(0xffffffffu, wt, (lane & ~3) | ((r & 7) >> 1));
-                if (c4 == col >> 1 && ((vis[mt][hf] >> r) & 1u)) {
-#pragma unroll
-                  for (int n = 0; n < F::VT; ++n)
-                    if (n == n_of) o[mt][n][2 * hf + (col & 1)] += wt * val;
+                  for (int j = 0; j < KT; ++j)
+                    if (j == jt) (hi ? o[j][n][2 + x] : o[j][n][x]) += wt * val;
                 }
-              }
+            }
           }
-          if (lane == src) {
-            uint32_t z = bw;
+          if (bad) {
             if (FP8) {
-              for (int b = 0; b < 4; ++b)
-                if (((bw >> (8 * b)) & 0x7fu) == 0x7fu) z &= ~(0xffu << (8 * b));
+              *word = w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
             } else {
-              if ((bw & 0x7f80u) == 0x7f80u) z &= 0xffff0000u;
-              if ((bw & 0x7f800000u) == 0x7f800000u) z &= 0xffffu;
+              *word = ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
+                      ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
             }
-            reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(sv))[be] = z;
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
-    }
 
-    // ---- O += P V ----
+      // ---- O^T += V^T P^T ----
+      const int mi = lane >> 3;
+      const uint32_t sva = smem_addr(sv);
 #pragma unroll
-    for (int tk = 0; tk < CH / 16; ++tk) {
-      uint32_t pf[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float(&x)[4] = s[mt][2 * tk];
-        const float(&y)[4] = s[mt][2 * tk + 1];
-        pf[mt][0] = FP8 ? f16x2(x[0], x[1]) : bf16x2(x[0], x[1]);
-        pf[mt][1] = FP8 ? f16x2(x[2], x[3]) : bf16x2(x[2], x[3]);
-        pf[mt][2] = FP8 ? f16x2(y[0], y[1]) : bf16x2(y[0], y[1]);
-        pf[mt][3] = FP8 ? f16x2(y[2], y[3]) : bf16x2(y[2], y[3]);
-      }
-      const int mtx = lane >> 3, vr = tk * 16 + (mtx & 1) * 8 + (lane & 7);
-#pragma unroll
-      for (int j = 0; j < F::CPR / 2; ++j) {
+      for (int j = 0; j < CPR / 2; ++j) {
         uint32_t r[4];
-        ldmatrix_x4_trans(r, smem_addr(sv + vr * RB + v_piece<RB>(vr, 2 * j + (mtx >> 1)) * 16));
+        const int vr = (FP8 ? mi & 1 : mi >> 1) * 8 + (lane & 7), pc = 2 * j + (FP8 ? mi >> 1 : mi & 1);
+        ldmatrix_x4_trans(r, sva + vr * RB + v_piece<RB>(vr, pc) * 16);
         if (FP8) {
-          // a register holds elements (2n, 2n+1) of tokens 2c and 2c+1: the
-          // even ones form one n-tile, the odd ones the next
+          // a register holds elements (2g, 2g + 1) of tokens 2c and 2c + 1:
+          // the even elements are rows 0..7 of an m-tile, the odd ones 8..15
 #pragma unroll
-          for (int dg = 0; dg < 2; ++dg) {
-            const uint32_t b0 = __byte_perm(r[2 * dg], 0, 0x3120), b1 = __byte_perm(r[2 * dg + 1], 0, 0x3120);
-            const uint32_t e0 = e4m3x2_to_f16x2((uint16_t)b0), e1 = e4m3x2_to_f16x2((uint16_t)b1);
-            const uint32_t o0 = e4m3x2_to_f16x2((uint16_t)(b0 >> 16)), o1 = e4m3x2_to_f16x2((uint16_t)(b1 >> 16));
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __byte_perm(r[2 * h], 0, 0x3120), hi = __byte_perm(r[2 * h + 1], 0, 0x3120);
+            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                                    e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_f16_16816(o[mt][4 * j + 2 * dg], pf[mt], e0, e1);
-              mma_f16_16816(o[mt][4 * j + 2 * dg + 1], pf[mt], o0, o1);
-            }
+            for (int n = 0; n < NR; ++n) mma_f16_16816(o[2 * j + h][n], af, pb[n][0], pb[n][1]);
           }
         } else {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16_16816(o[mt][2 * j], pf[mt], r[0], r[1]);
-            mma_bf16_16816(o[mt][2 * j + 1], pf[mt], r[2], r[3]);
-          }
+          for (int n = 0; n < NR; ++n) mma_bf16_16816(o[j][n], r, pb[n][0], pb[n][1]);
         }
       }
     }
-  }
-  cp_async_wait<0>();
-  __syncthreads();  // every ring is free: its memory takes the warps' results
+    cp_async_wait<0>();
+    __syncthreads();  // every ring is free: its memory takes the warps' results
 
-  // ---- join the warps ----
-  float *so = reinterpret_cast<float *>(smem);                              // [NW][R][DH]
-  float4 *sml = reinterpret_cast<float4 *>(smem + (size_t)NW * R * DH * 4);  // [NW][R]
+    // ---- join the warps ----
+    float *so = reinterpret_cast<float *>(smem);                                      // [NW][R][OROW]
+    float4 *sml = reinterpret_cast<float4 *>(smem + (size_t)NW * R * F::OROW * 4);  // [NW][R]
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float l = l_run[mt][hf];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int r = mt * 16 + g + 8 * hf;
-      if (c4 == 0) sml[warp * R + r] = make_float4(m_run[mt][hf], l, y_run[mt][hf], 0.f);
-      float *row = so + ((size_t)warp * R + r) * DH;
+      for (int x = 0; x < 2; ++x) {
+        float l = l_sum[n][x];
 #pragma unroll
-      for (int n = 0; n < F::VT; ++n) {
-        if (FP8) {
-          // n-tiles 2j and 2j+1: elements 16j + 4c4 + {0, 2} and {1, 3}
-          if ((n & 1) == 0)
-            *reinterpret_cast<float4 *>(row + 8 * n + 4 * c4) =
-                make_float4(o[mt][n][2 * hf], o[mt][n | 1][2 * hf], o[mt][n][2 * hf + 1], o[mt][n | 1][2 * hf + 1]);
-        } else {
-          *reinterpret_cast<float2 *>(row + 8 * n + 2 * c4) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+        for (int b = 4; b < 32; b <<= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+        const int r = warp * R + n * 8 + 2 * c4 + x;
+        if (g == 0) sml[r] = make_float4(m_ref[n][x], l, y_ref[n][x], 0.f);
+        float *row = so + (size_t)r * F::OROW;
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          if (FP8) {
+            *reinterpret_cast<float2 *>(row + 16 * j + 2 * g) = make_float2(o[j][n][x], o[j][n][2 + x]);
+          } else {
+            row[16 * j + g] = o[j][n][x];
+            row[16 * j + 8 + g] = o[j][n][2 + x];
+          }
         }
       }
-    }
-  __syncthreads();
-  for (int e = tid; e < R * (DH / 4); e += THREADS) {
-    const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
-    const int q = rows.query[r];
-    if (q < 0) continue;
-    float M = NEG_INF, Y = NEG_INF;
+    __syncthreads();
+    for (int e = tid; e < n_rows * (DH / 4); e += F::THREADS) {
+      const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
+      float M = NEG_INF, Y = NEG_INF;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      M = fmaxf(M, sml[w * R + r].x);
-      Y = fmaxf(Y, sml[w * R + r].z);
-    }
-    const float ref = M == NEG_INF ? 0.f : M, yref = Y == NEG_INF ? 0.f : Y;
-    float l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < NW; ++w) {
+        M = fmaxf(M, sml[w * R + r].x);
+        Y = fmaxf(Y, sml[w * R + r].z);
+      }
+      const float ref = M == NEG_INF ? 0.f : M, yref = Y == NEG_INF ? 0.f : Y;
+      float l = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float4 ml = sml[w * R + r];
-      const float f = ex2(ml.z - yref);
-      const float4 x = *reinterpret_cast<const float4 *>(so + ((size_t)w * R + r) * DH + d0);
-      l = fmaf(ml.y, ex2(ml.x - ref), l);
-      v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+      for (int w = 0; w < NW; ++w) {
+        const float4 ml = sml[w * R + r];
+        const float f = ex2(ml.z - yref);
+        const float4 x = *reinterpret_cast<const float4 *>(so + ((size_t)w * R + r) * F::OROW + d0);
+        l = fmaf(ml.y, ex2(ml.x - ref), l);
+        v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+      }
+      const int64_t orow = (int64_t)row_query(r) * a.H + row_head(r);
+      if (Z > 1) {
+        const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
+        *reinterpret_cast<float4 *>(split.o + prow * DH + d0) = v;
+        if (d0 == 0) split.ml[prow] = make_float4(M, l, Y, 0.f);
+      } else {
+        const bool none = M == NEG_INF && l == 0.f;
+        const float inv = none ? 0.f : ex2(yref - ref) / l;
+        *reinterpret_cast<uint2 *>(a.out + orow * DH + d0) =
+            make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
+        if (a.lse && d0 == 0) a.lse[orow] = none ? NEG_INF : M * LN2 + logf(l);
+      }
     }
-    const int64_t orow = (int64_t)q * a.H + row_head(r);
-    if (Z > 1) {
-      const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
-      *reinterpret_cast<float4 *>(split.o + prow * DH + d0) = v;
-      if (d0 == 0) split.ml[prow] = make_float4(M, l, Y, 0.f);
-    } else {
-      const bool none = M == NEG_INF && l == 0.f;
-      const float inv = none ? 0.f : ex2(yref - ref) / l;
-      *reinterpret_cast<uint2 *>(a.out + orow * DH + d0) =
-          make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
-      if (a.lse && d0 == 0) a.lse[orow] = none ? NEG_INF : M * LN2 + logf(l);
-    }
+    if (LIST) break;
+    __syncthreads();
+    tile_i += tile_step;
+    t = find_tile<F::THREADS>(a, per, tile_i);
   }
 }
 
@@ -691,45 +752,56 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(AttendView a, Split
 }
 
 struct Plan {
-  int mt, tiles, tiles_per_query, Z;
+  int nr;         // n-tiles of 8 rows per CTA
+  int per;        // queries per tile (1 with lists)
+  int row_tiles;  // tiles of a query's G rows (per == 1)
+  int tiles, Z;
 };
 
-// The most chunks a CTA row tile can have (lengths are on the device: whole
-// prefixes count as full caches).
-Plan make_plan(int n_q, int H, int H_kv, int L_cap, bool fp8, int k, int n_draft) {
+// Rows of a tile: as many n-tiles as one query's G heads (and, without lists,
+// its sequence's neighbours) fill, 32 rows at the most.  Lengths are on the
+// device: whole prefixes count as full caches, and the batch's queries as
+// spread evenly over the sequences.
+Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   Plan p;
-  const int G = H / H_kv;
+  const int G = H / c.H_kv;
   const bool list = k > 0;
-  const int64_t rows = list ? G : (int64_t)n_q * G;
-  p.mt = rows > 16 ? 2 : 1;
-  const int R = 16 * p.mt, CH = fp8 ? 32 : 16;
-  p.tiles_per_query = list ? cdiv(G, R) : 0;
-  p.tiles = list ? n_q * p.tiles_per_query : (int)((rows + R - 1) / R);
-  const int chunks = cdiv(list ? k : L_cap, CH) + cdiv(n_draft, CH);
-  const int64_t ctas = (int64_t)p.tiles * H_kv;
+  const int seqs = std::max(1, std::min(n_q, c.n_seq)), per_seq = cdiv(std::max(n_q, 1), seqs);
+  const int rows = list ? G : G * std::min(per_seq, 32);
+  p.nr = rows > 16 ? 4 : rows > 8 ? 2 : 1;
+  const int R = 8 * p.nr;
+  p.per = list ? 1 : std::max(1, R / G);
+  p.row_tiles = p.per > 1 ? 1 : cdiv(G, R);
+  p.tiles = list ? n_q : std::min(n_q, cdiv(n_q, p.per) + seqs);
+  const int tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
+  const int chunks = cdiv(list ? k : c.L_cap, CH) + cdiv(n_draft, CH);
+  const int nw = c.fp8 ? 8 : 4, ctas = ctas_per_sm(c.fp8, c.d, p.nr);
+  const int64_t units = (int64_t)tiles * p.row_tiles * c.H_kv;
   // shares: fill the SMs once, two chunks per warp at the least
-  const int64_t want = ctas > 0 ? device_sms() / ctas : 1;
-  p.Z = (int)std::max<int64_t>(1, std::min<int64_t>(want, chunks / (2 * NW)));
+  const int64_t want = units > 0 ? (int64_t)device_sms() * ctas / units : 1;
+  p.Z = (int)std::max<int64_t>(1, std::min<int64_t>(want, chunks / (2 * nw)));
   return p;
 }
 
-template <int DH, bool FP8, int MT, bool LIST>
+template <class F, bool LIST>
 cudaError_t run_attend(const KvView &c, const AttendView &a, const Split &sp, const Plan &p, cudaStream_t s) {
-  using F = Cfg<DH, FP8>;
-  constexpr size_t ring = (size_t)NW * STAGES * F::STAGE, join = (size_t)NW * 16 * MT * (DH * 4 + 16);
-  constexpr size_t bytes = ring > join ? ring : join;
   struct Tag {};
-  const int have = cached_per_device<Tag>([] { return opt_in_max_dyn_smem(attend_kernel<DH, FP8, MT, LIST>); });
-  if (have < (int)bytes) return cudaErrorInvalidConfiguration;
-  return launch_kernel(attend_kernel<DH, FP8, MT, LIST>, dim3(p.tiles, c.H_kv, p.Z), dim3(THREADS), bytes, s, c, a, sp,
-                       p.tiles_per_query);
+  const int have = cached_per_device<Tag>([] { return opt_in_max_dyn_smem(attend_kernel<F, LIST>); });
+  if (have < (int)F::SMEM) return cudaErrorInvalidConfiguration;
+  return launch_kernel(attend_kernel<F, LIST>, dim3((unsigned)(p.tiles * p.row_tiles), c.H_kv, p.Z), dim3(F::THREADS),
+                       F::SMEM, s, c, a, sp, p.per, p.row_tiles);
+}
+
+template <int DH, bool FP8, bool LIST>
+cudaError_t pick_rows(const KvView &c, const AttendView &a, const Split &sp, const Plan &p, cudaStream_t s) {
+  return p.nr == 1   ? run_attend<Cfg<DH, FP8, 1>, LIST>(c, a, sp, p, s)
+         : p.nr == 2 ? run_attend<Cfg<DH, FP8, 2>, LIST>(c, a, sp, p, s)
+                     : run_attend<Cfg<DH, FP8, 4>, LIST>(c, a, sp, p, s);
 }
 
 template <int DH, bool FP8>
 cudaError_t pick_attend(const KvView &c, const AttendView &a, const Split &sp, const Plan &p, cudaStream_t s) {
-  if (a.topk)
-    return p.mt == 2 ? run_attend<DH, FP8, 2, true>(c, a, sp, p, s) : run_attend<DH, FP8, 1, true>(c, a, sp, p, s);
-  return p.mt == 2 ? run_attend<DH, FP8, 2, false>(c, a, sp, p, s) : run_attend<DH, FP8, 1, false>(c, a, sp, p, s);
+  return a.topk ? pick_rows<DH, FP8, true>(c, a, sp, p, s) : pick_rows<DH, FP8, false>(c, a, sp, p, s);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -737,7 +809,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
 size_t attend_ws_bytes(const KvView &c, int n_q, int H, int k, int n_draft) {
-  const Plan p = make_plan(n_q, H, c.H_kv, c.L_cap, c.fp8, k, n_draft);
+  const Plan p = make_plan(c, n_q, H, k, n_draft);
   if (p.Z <= 1) return 0;
   const size_t n = (size_t)p.Z * n_q * H;
   return round256(n * c.d * 4) + round256(n * 16);
@@ -745,7 +817,7 @@ size_t attend_ws_bytes(const KvView &c, int n_q, int H, int k, int n_draft) {
 
 cudaError_t launch_attend(const KvView &c, const AttendView &a, void *ws, cudaStream_t s) {
   if (a.n_q == 0) return cudaSuccess;
-  const Plan p = make_plan(a.n_q, a.H, c.H_kv, c.L_cap, c.fp8, a.topk ? a.k : 0, a.n_draft);
+  const Plan p = make_plan(c, a.n_q, a.H, a.topk ? a.k : 0, a.n_draft);
   Split sp = {nullptr, nullptr, p.Z};
   if (p.Z > 1) {
     sp.o = static_cast<float *>(ws);
