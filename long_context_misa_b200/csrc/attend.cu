@@ -32,6 +32,7 @@
 // row's largest contribution lies in [2^-8, 2^8]: the largest contribution
 // sets f16's range, not the largest scale.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 
@@ -39,8 +40,7 @@ namespace misa {
 namespace {
 
 constexpr int CH = 16;  // tokens per chunk
-constexpr int STAGES = 3;
-constexpr float LAZY = 8.f;  // base-2 headroom of the running maximum
+constexpr float LAZY = 256.f;  // most that a weight may reach before its reference moves
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NEG_INF = -__builtin_huge_valf();
@@ -66,6 +66,14 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
+// Four e4m3 codes -> their exact f16 values, two to a register.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -83,8 +91,15 @@ __device__ __forceinline__ float row_scale(float amax) {
   return ldexpf(1.f, min(max(e, -126), 126));
 }
 
+// Warps per CTA, CTAs per SM and chunks in a warp's ring: as many warps as the
+// registers of their O (32 per n-tile and d = 128) allow, their rings sharing
+// the SM's shared memory.
+constexpr int NW = 4;
 __host__ __device__ constexpr int ctas_per_sm(bool fp8, int d, int nr) {
-  return fp8 ? (nr > 2 ? 1 : 2) : d > 64 ? 2 : nr > 2 ? 3 : 4;
+  return nr > 2 ? 2 : fp8 ? (nr > 1 && d > 64 ? 3 : 4) : d > 64 ? 2 : 4;
+}
+__host__ __device__ constexpr int ring_chunks(bool fp8, int d, int nr) {
+  return fp8 && d > 64 ? (nr > 2 ? 6 : nr > 1 ? 4 : 3) : fp8 || d == 64 ? (nr > 2 ? 4 : 3) : 3;
 }
 
 template <int DH_, bool FP8_, int NR_>
@@ -95,11 +110,7 @@ struct Cfg {
   static constexpr int CPR = RB / 16;            // 16-byte pieces per row
   static constexpr int KT = DH / 16;             // k-tiles of S, m-tiles of O
   static constexpr int STAGE = 2 * CH * RB + (FP8 ? 2 * CH * 4 : 0);  // keys, values, their scales
-  // Warps per CTA and CTAs per SM: 16 warps of an e4m3 kernel (whose codes
-  // are widened in registers) or 8 of a bf16 one fill the SM's shared memory
-  // with their rings; 32 rows take the registers of 8 warps.
-  static constexpr int NW = FP8 ? 8 : 4;
-  static constexpr int CTAS = ctas_per_sm(FP8, DH, NR);
+  static constexpr int CTAS = ctas_per_sm(FP8, DH, NR), STAGES = ring_chunks(FP8, DH, NR);
   static constexpr int THREADS = NW * 32;
   static constexpr int R = 8 * NR;
   static constexpr int OROW = DH + 8;  // floats between rows of a warp's result
@@ -234,11 +245,12 @@ template <class F, bool LIST>
 __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     attend_kernel(KvView c, AttendView a, Split split, int per, int row_tiles) {
   grid_dep_sync();
-  constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT, NW = F::NW;
+  constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT;
   constexpr bool FP8 = F::FP8;
+  constexpr int STAGES = F::STAGES;
   constexpr bool Q_SMEM = NR > (FP8 ? 1 : 2);  // the query fragments do not fit beside O
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint2 q_s[Q_SMEM ? KT * NR * 32 : 1];
+  __shared__ __align__(16) uint2 q_s[Q_SMEM ? KT * NR * 32 : 1];  // [k-tile][pair of n-tiles][lane][2]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
   const int G = a.H / c.H_kv, hk = blockIdx.y, Z = split.Z;
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         for (int u = 0; u < 2; ++u) {
           const uint2 v = make_uint2(w[2 * u], w[2 * u + 1]);
           if (Q_SMEM)
-            q_s[((2 * i + u) * NR + n) * 32 + lane] = v;
+            q_s[(((2 * i + u) * (NR / 2) + n / 2) * 32 + lane) * 2 + (n & 1)] = v;
           else
             qf[2 * i + u][n] = v;
         }
@@ -411,45 +423,67 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       return tok * c.H_kv + hk;
     };
     // Gather a chunk's rows into stage st; returns which tokens are there.
-    auto issue = [&](int st, int row) -> uint32_t {
+    // The lane takes piece pc of rows q0r, q0r + RPI, ...; a full chunk (the
+    // usual one) copies without predicates.
+    constexpr int RPI = 32 / CPR;
+    const int q0r = lane / CPR, pc = lane % CPR;
+    const uint8_t *kl = kb + pc * 16, *vl = vb + pc * 16;
+    const uint32_t dk = ring_a + q0r * RB + k_piece<RB>(q0r, pc) * 16, dv = ring_a + CH * RB + q0r * RB;
+    const uint32_t v0 = v_piece<RB>(q0r, pc) * 16;
+    auto issue = [&](int at, int row) -> uint32_t {
       const uint32_t have = __ballot_sync(0xffffffffu, row >= 0) & ALL;
-      if (have) {
-        const uint32_t sk = ring_a + st * F::STAGE, sv = sk + CH * RB;
+      auto copy = [&](auto &&put) {
 #pragma unroll
-        for (int it = 0; it < CH * CPR / 32; ++it) {
-          const int r = it * (32 / CPR) + lane / CPR, pc = lane % CPR;
-          const int x = __shfl_sync(0xffffffffu, row, r);
-          const int64_t off = (int64_t)(max(x, 0) * CPR + pc) * 16;  // below 2^29 pieces
-          cp_async16(sk + r * RB + k_piece<RB>(r, pc) * 16, kb + off, x >= 0);
-          cp_async16(sv + r * RB + v_piece<RB>(r, pc) * 16, vb + off, x >= 0);
+        for (int it = 0; it < CH / RPI; ++it) {
+          const int x = __shfl_sync(0xffffffffu, max(row, 0), it * RPI + q0r);
+          const uint64_t off = (uint64_t)(uint32_t)x * RB;
+          // (the bits of it * RPI and of q0r do not meet)
+          put(it, dk + at + it * RPI * RB, kl + off, dv + at + it * RPI * RB + (v0 ^ v_piece<RB>(it * RPI, 0) * 16), vl + off);
         }
-        if (FP8) cp_async4(sv + CH * RB + lane * 4, (lane < CH ? c.k_scale : c.v_scale) + sb + max(row, 0), row >= 0);
+      };
+      static_assert(RPI % 2 == 0, "k_piece's row parity");
+      if (have == ALL) {
+        copy([&](int, uint32_t ka, const uint8_t *ks, uint32_t va, const uint8_t *vs) {
+          cp_async16(ka, ks);
+          cp_async16(va, vs);
+        });
+      } else if (have) {
+        copy([&](int it, uint32_t ka, const uint8_t *ks, uint32_t va, const uint8_t *vs) {
+          const bool there = (have >> (it * RPI + q0r)) & 1u;
+          cp_async16(ka, ks, there);
+          cp_async16(va, vs, there);
+        });
       }
+      if (FP8 && have)
+        cp_async4(ring_a + at + 2 * CH * RB + lane * 4, (lane < CH ? c.k_scale : c.v_scale) + sb + max(row, 0),
+                  row >= 0);
       cp_async_commit();
       return have;
     };
 
     int nxt = cb + warp;
     int row_n = row_of(nxt);
-    uint32_t have_q[STAGES];
+    uint32_t have_q[STAGES - 1];
 #pragma unroll
     for (int st = 0; st < STAGES - 1; ++st) {
-      have_q[st] = issue(st, row_n);
+      have_q[st] = issue(st * F::STAGE, row_n);
       nxt += NW;
       row_n = row_of(nxt);
     }
-    int st = 0;
+    int at = 0, put_at = (STAGES - 1) * F::STAGE;  // stage read now, stage written now
     for (int ck = cb + warp; ck < ce; ck += NW) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();  // every lane's copies have landed, and its reads of the stage issued next are done
       const uint32_t have = have_q[0];
-      have_q[0] = have_q[1];
-      have_q[1] = issue(st == 0 ? STAGES - 1 : st - 1, row_n);
+#pragma unroll
+      for (int st = 0; st < STAGES - 2; ++st) have_q[st] = have_q[st + 1];
+      have_q[STAGES - 2] = issue(put_at, row_n);
       nxt += NW;
       row_n = row_of(nxt);
-      uint8_t *sk = ring + st * F::STAGE, *sv = sk + CH * RB;
+      uint8_t *sk = ring + at, *sv = sk + CH * RB;
       const float *ss = reinterpret_cast<const float *>(sv + CH * RB);
-      st = st == STAGES - 1 ? 0 : st + 1;
+      put_at = at;
+      at = at == (STAGES - 1) * F::STAGE ? 0 : at + F::STAGE;
       if (!have) continue;
 
       // ---- S^T = K Q^T ----
@@ -466,77 +500,106 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           const int kt = ch * (FP8 ? 4 : 2) + u;
           uint32_t af[4];
           if (FP8) {
-            af[0] = e4m3x2_to_f16x2((uint16_t)wa[u]), af[1] = e4m3x2_to_f16x2((uint16_t)wb[u]);
-            af[2] = e4m3x2_to_f16x2((uint16_t)(wa[u] >> 16)), af[3] = e4m3x2_to_f16x2((uint16_t)(wb[u] >> 16));
+            widen(wa[u], af[0], af[2]);
+            widen(wb[u], af[1], af[3]);
           } else {
             af[0] = wa[2 * u], af[1] = wb[2 * u], af[2] = wa[2 * u + 1], af[3] = wb[2 * u + 1];
           }
+          if (Q_SMEM) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n) {
-            const uint2 q = Q_SMEM ? q_s[(kt * NR + n) * 32 + lane] : qf[Q_SMEM ? 0 : kt][Q_SMEM ? 0 : n];
-            if (FP8)
-              mma_f16_16816(s[n], af, q.x, q.y);
-            else
-              mma_bf16_16816(s[n], af, q.x, q.y);
+            for (int n = 0; n < NR; n += 2) {
+              const uint4 q = *reinterpret_cast<const uint4 *>(q_s + ((kt * (NR / 2) + n / 2) * 32 + lane) * 2);
+              FP8 ? mma_f16_16816(s[n], af, q.x, q.y) : mma_bf16_16816(s[n], af, q.x, q.y);
+              FP8 ? mma_f16_16816(s[n + 1], af, q.z, q.w) : mma_bf16_16816(s[n + 1], af, q.z, q.w);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              const uint2 q = qf[Q_SMEM ? 0 : kt][Q_SMEM ? 0 : n];
+              FP8 ? mma_f16_16816(s[n], af, q.x, q.y) : mma_bf16_16816(s[n], af, q.x, q.y);
+            }
           }
         }
       }
 
-      // ---- base-2 logits of the tokens g and g + 8 (index y), columns x;
-      // what is not seen becomes -inf ----
-      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-      if (FP8) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          ks[y] = ss[g + 8 * y];
-          vs[y] = ss[CH + g + 8 * y];
-          lv[y] = __log2f(vs[y] < 0x1p-100f ? 0x1p-100f : vs[y]);  // a NaN stays
-        }
-      }
+      // ---- what each column sees of the chunk ----
       uint32_t vis[NR][2];
-      bool mixed = false;  // some row does not see a gathered token
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t v = have;
-          if (!LIST) {
-            const int r = n * 8 + 2 * c4 + x;
-            if (col_len[n][x] < 0) {
-              v = 0u;
-            } else if (ck < c1) {
-              const int nn = col_len[n][x] - ck * CH;
-              v &= nn >= CH ? ALL : nn > 0 ? (1u << nn) - 1u : 0u;
-            } else {
-              const int j0 = (ck - c1) * CH;
-              uint32_t m = a.draft_mask[(int64_t)row_query(r) * words + (j0 >> 5)] >> (j0 & 31) & ALL;
-              if (a.n_draft - j0 < CH) m &= (1u << (a.n_draft - j0)) - 1u;
-              if (m & ~have) flag(c, MISA_DEV_BAD_POSITION);
-              v &= m;
-            }
-            mixed |= col_len[n][x] >= 0 && v != have;
-          }
-          vis[n][x] = v;
-        }
-      bool above = false;
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float &v = s[n][2 * y + x];
-            v *= FP8 ? ks[y] * mul[n][x] : mul[n][x];
-            if ((!LIST || have != ALL) && !((vis[n][x] >> (g + 8 * y)) & 1u)) v = NEG_INF;
-            above |= v > m_ref[n][x] + LAZY;
-            if (FP8) above |= v + lv[y] > y_ref[n][x] + LAZY;
-          }
-      if (__any_sync(0xffffffffu, above)) {
+      bool masked = have != ALL, mixed = false;  // something is not seen; by some row only
+      if (!LIST) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = fmaxf(s[n][x], s[n][2 + x]), my = fmaxf(s[n][x] + lv[0], s[n][2 + x] + lv[1]);
+            uint32_t v = have;
+            const int r = n * 8 + 2 * c4 + x;
+            if (r < n_rows) {
+              if (col_len[n][x] < 0) {
+                v = 0u;
+              } else if (ck < c1) {
+                const int nn = col_len[n][x] - ck * CH;
+                v &= nn >= CH ? ALL : nn > 0 ? (1u << nn) - 1u : 0u;
+              } else {
+                const int j0 = (ck - c1) * CH;
+                uint32_t m = a.draft_mask[(int64_t)row_query(r) * words + (j0 >> 5)] >> (j0 & 31) & ALL;
+                if (a.n_draft - j0 < CH) m &= (1u << (a.n_draft - j0)) - 1u;
+                if (m & ~have) flag(c, MISA_DEV_BAD_POSITION);
+                v &= m;
+              }
+            }
+            mixed |= v != have;
+            vis[n][x] = v;
+          }
+        mixed = __any_sync(0xffffffffu, mixed);
+        masked |= mixed;
+      }
+
+      // ---- weights of the tokens g and g + 8 (index y) for the columns x:
+      // p = e^(s - ref) for the sum, w for the values ----
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+      if (FP8) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) ks[y] = ss[g + 8 * y], vs[y] = ss[CH + g + 8 * y];
+      }
+      float p[NR][4], w[NR][4];
+      auto logit = [&](auto m, float v, int n, int x, int y) {
+        return m.value && !(((LIST ? have : vis[n][x]) >> (g + 8 * y)) & 1u) ? NEG_INF : v;
+      };
+      auto weigh = [&](auto m) -> bool {  // m: std::true_type where something is masked
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int e = 2 * y + x;
+              const float v = logit(m, fmaf(s[n][e], FP8 ? ks[y] * mul[n][x] : mul[n][x], -m_ref[n][x]), n, x, y);
+              p[n][e] = ex2(v);
+              w[n][e] = p[n][e];
+              if (FP8) {
+                w[n][e] *= vs[y] * fac[n][x];
+                // (rows gathered for others may hold any scale)
+                if (!LIST && m.value && v == NEG_INF) w[n][e] = 0.f;
+              }
+              top = fmaxf(top, fmaxf(p[n][e], w[n][e]));
+            }
+        return __any_sync(0xffffffffu, top > LAZY);
+      };
+      for (bool again = false;; again = true) {
+        const bool above = masked ? weigh(std::true_type()) : weigh(std::false_type());
+        // the first chunk comes here with ref = -inf, p = inf
+        if (again || !above) break;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = NEG_INF, my = NEG_INF;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float v = logit(std::true_type(), s[n][2 * y + x] * (FP8 ? ks[y] * mul[n][x] : mul[n][x]), n, x, y);
+              mx = fmaxf(mx, v);
+              if (FP8) my = fmaxf(my, v + __log2f(vs[y] < 0x1p-100f ? 0x1p-100f : vs[y]));  // a NaN stays
+            }
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) {
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
@@ -558,37 +621,26 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float ref = m_ref[n][x] == NEG_INF ? 0.f : m_ref[n][x];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float &v = s[n][2 * y + x];
-            // (rows gathered for others may hold any scale)
-            const bool seen = LIST || v != NEG_INF;
-            v = ex2(v - ref);
-            l_sum[n][x] += v;
-            if (FP8) v = seen ? v * (vs[y] * fac[n][x]) : 0.f;
-          }
-        }
+        for (int x = 0; x < 2; ++x) l_sum[n][x] += p[n][x] + p[n][2 + x];
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          pb[n][y] = movmatrix_trans(FP8 ? f16x2(s[n][2 * y], s[n][2 * y + 1]) : bf16x2(s[n][2 * y], s[n][2 * y + 1]));
+          pb[n][y] = movmatrix_trans(FP8 ? f16x2(w[n][2 * y], w[n][2 * y + 1]) : bf16x2(w[n][2 * y], w[n][2 * y + 1]));
       }
 
       // ---- values that some rows must not see: a NaN or infinity there would
       // reach them as 0 * NaN.  Such values are taken out of the chunk and
       // added to the rows that do see them ----
-      if (!LIST && __any_sync(0xffffffffu, mixed)) {
+      if (!LIST && mixed) {
         for (int e = lane; e < CH * RB / 4; e += 32) {
           uint32_t *word = reinterpret_cast<uint32_t *>(sv) + e;
-          const uint32_t w = *word;
-          const bool bad = FP8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u
-                               : (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+          const uint32_t cw = *word;
+          const bool bad = FP8 ? __vcmpeq4(cw & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u
+                               : (cw & 0x7f80u) == 0x7f80u || (cw & 0x7f800000u) == 0x7f800000u;
           uint32_t who = __ballot_sync(0xffffffffu, bad);
           while (who) {
             const int src = __ffs(who) - 1;
             who &= who - 1;
-            const uint32_t bw = __shfl_sync(0xffffffffu, w, src);
+            const uint32_t bw = __shfl_sync(0xffffffffu, cw, src);
             const int at = (e - lane + src) * 4, r = at / RB, off = at % RB;
             const int d0 = (v_piece<RB>(r, off >> 4) * 16 + (off & 15)) / (FP8 ? 1 : 2);
             for (int b = 0; b < (FP8 ? 4 : 2); ++b) {
@@ -601,7 +653,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
               for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const float wt = __shfl_sync(0xffffffffu, r < 8 ? s[n][x] : s[n][2 + x], (r & 7) * 4 + c4);
+                  const float wt = __shfl_sync(0xffffffffu, r < 8 ? w[n][x] : w[n][2 + x], (r & 7) * 4 + c4);
                   if (g != gt || !((vis[n][x] >> r) & 1u)) continue;
 #pragma unroll
                   for (int j = 0; j < KT; ++j)
@@ -611,10 +663,10 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           }
           if (bad) {
             if (FP8) {
-              *word = w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              *word = cw & ~__vcmpeq4(cw & 0x7f7f7f7fu, 0x7f7f7f7fu);
             } else {
-              *word = ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) |
-                      ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+              *word = ((cw & 0x7f80u) == 0x7f80u ? 0u : cw & 0xffffu) |
+                      ((cw & 0x7f800000u) == 0x7f800000u ? 0u : cw & 0xffff0000u);
             }
           }
         }
@@ -634,9 +686,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           // the even elements are rows 0..7 of an m-tile, the odd ones 8..15
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __byte_perm(r[2 * h], 0, 0x3120), hi = __byte_perm(r[2 * h + 1], 0, 0x3120);
-            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
-                                    e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+            uint32_t af[4];
+            widen(__byte_perm(r[2 * h], 0, 0x3120), af[0], af[1]);
+            widen(__byte_perm(r[2 * h + 1], 0, 0x3120), af[2], af[3]);
 #pragma unroll
             for (int n = 0; n < NR; ++n) mma_f16_16816(o[2 * j + h][n], af, pb[n][0], pb[n][1]);
           }
@@ -775,11 +827,11 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   p.tiles = list ? n_q : std::min(n_q, cdiv(n_q, p.per) + seqs);
   const int tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
   const int chunks = cdiv(list ? k : c.L_cap, CH) + cdiv(n_draft, CH);
-  const int nw = c.fp8 ? 8 : 4, ctas = ctas_per_sm(c.fp8, c.d, p.nr);
+  const int ctas = ctas_per_sm(c.fp8, c.d, p.nr);
   const int64_t units = (int64_t)tiles * p.row_tiles * c.H_kv;
   // shares: fill the SMs once, two chunks per warp at the least
   const int64_t want = units > 0 ? (int64_t)device_sms() * ctas / units : 1;
-  p.Z = (int)std::max<int64_t>(1, std::min<int64_t>(want, chunks / (2 * nw)));
+  p.Z = (int)std::max<int64_t>(1, std::min<int64_t>(want, chunks / (2 * NW)));
   return p;
 }
 
