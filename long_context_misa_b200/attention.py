@@ -89,26 +89,33 @@ def _need(ok: bool, what: str, kind=ValueError) -> None:
         raise kind(what)
 
 
-def _ints(t: torch.Tensor, n: int, what: str, device) -> torch.Tensor:
-    """A contiguous int32 tensor of n elements on the device."""
-    if t.dtype != torch.int32:
+def _ints(t: torch.Tensor, n: int, what: str, device) -> None:
+    """A contiguous int32 tensor of n elements on the device.  (Messages are built only for a refusal: formatting
+    them costs more than the checks.)"""
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
-    _need(t.numel() == n and t.is_contiguous(), f"{what} must be contiguous with {n} entries, got {tuple(t.shape)}")
-    _on(t, device, what)
-    return t
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} entries, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
 
 
 def _on(t: torch.Tensor, device, what: str) -> None:
-    _need(t.device == device, f"{what} is on {t.device}, expected {device}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
 
 
 def _call(fn, device, stream, *args) -> None:
-    """fn(*args, stream) with `device` current."""
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _m._check(fn(*args, _m._stream(stream)))
+    """fn(*args, stream) with `device` current; the default is the device's current stream."""
+    if device.type != "cuda":
+        st = fn(*args, None if stream is None else _m._stream(stream))
+    elif device.index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _m._stream(stream))
     else:
-        _m._check(fn(*args, _m._stream(stream)))
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _m._stream(stream))
+    if st:
+        _m._check(st)
 
 
 def _allocating(stream):
@@ -148,6 +155,7 @@ class Rope:
         self.rot, self.first, self.layout, self.amplitude = int(rot), int(first), layout, float(amplitude)
         self.phases = phases.to(device).contiguous()
         self._s = misa_rope(_m._ptr(self.phases), self.rot, self.first, ROPE_LAYOUTS[layout], self.amplitude)
+        self._p = ctypes.byref(self._s)
 
     @property
     def struct(self) -> misa_rope:
@@ -160,21 +168,26 @@ def apply_rope(rope: Rope, rows: Sequence[Tuple[torch.Tensor, torch.Tensor, torc
     rows: (x, pos, out) triples; x and out are bf16 (or bf16 bits) [n][H][d] with consecutive elements along d and
     any other strides, out may be x itself; pos is int32 [n].
     """
-    _need(1 <= len(rows) <= MAX_ROPE_GROUPS, f"apply_rope takes 1 to {MAX_ROPE_GROUPS} tensors, got {len(rows)}")
+    if not 1 <= len(rows) <= MAX_ROPE_GROUPS:
+        raise ValueError(f"apply_rope takes 1 to {MAX_ROPE_GROUPS} tensors, got {len(rows)}")
     groups = (misa_rope_rows * len(rows))()
     device = rope.phases.device
-    for g, (x, pos, out) in zip(groups, rows):
-        if x.dtype not in _BF16 or out.dtype != x.dtype:
+    for i, (x, pos, out) in enumerate(rows):
+        if x.dtype not in _BF16 or out.dtype is not x.dtype:
             raise TypeError(f"rows must be bf16 and of one type, got {x.dtype} and {out.dtype}")
-        _need(x.dim() == 3 and x.shape == out.shape, f"rows must be [n][H][d], got {tuple(x.shape)}, {tuple(out.shape)}")
-        sx, sy, shape = x.stride(), out.stride(), x.shape
-        _need(shape[2] < 2 or (sx[2] == 1 and sy[2] == 1), "the elements of a row must be consecutive")
-        _on(x, device, "x"), _on(out, device, "out")
-        _ints(pos, shape[0], "pos", device)
-        g.x, g.y, g.pos = x.data_ptr(), out.data_ptr(), pos.data_ptr()
-        g.x_row, g.x_head, g.y_row, g.y_head = sx[0], sx[1], sy[0], sy[1]
-        g.n, g.H, g.d = shape
-    _call(_lib.misa_apply_rope, device, stream, ctypes.byref(rope.struct), groups, len(rows))
+        shape = x.shape
+        if len(shape) != 3 or out.shape != shape:
+            raise ValueError(f"rows must be [n][H][d], got {tuple(shape)}, {tuple(out.shape)}")
+        n, H, d = shape
+        x_row, x_head, x_el = x.stride()
+        y_row, y_head, y_el = out.stride()
+        if (x_el != 1 or y_el != 1) and d > 1:
+            raise ValueError("the elements of a row must be consecutive")
+        if x.device != device or out.device != device:
+            raise ValueError(f"rows are on {x.device} and {out.device}, the phases on {device}")
+        _ints(pos, n, "pos", device)
+        groups[i] = (x.data_ptr(), out.data_ptr(), pos.data_ptr(), x_row, x_head, y_row, y_head, n, H, d)
+    _call(_lib.misa_apply_rope, device, stream, rope._p, groups, len(rows))
 
 
 class KVCache:
@@ -212,6 +225,7 @@ class KVCache:
         _ints(self.status, 1, "status", k.device)
         self._s = misa_kv(_m._ptr(k), _m._ptr(v), _m._ptr(k_scale), _m._ptr(v_scale), _m._ptr(seq_len),
                           _m._ptr(self.status), self.n_seq, self.L_cap, self.H_kv, self.d, self.dtype)
+        self._p = ctypes.byref(self._s)
 
     @classmethod
     def empty(cls, n_seq: int, L_cap: int, H_kv: int, d: int = 128, e4m3: bool = True, device="cuda") -> "KVCache":
@@ -236,49 +250,49 @@ def append_kv(kv: KVCache, new_k: torch.Tensor, new_v: torch.Tensor, new_pos: to
     """Write new_k, new_v (bf16 [n_seq][count][H_kv][d], consecutive along d) at new_pos [n_seq], the keys rotated
     by rope at rope_pos [n_seq][count] (default: the positions written) and quantised to the cache's type.
     commit=False leaves seq_len (drafted tokens)."""
-    n = misa_new_kv()
-    want = (kv.n_seq, kv.H_kv, kv.d)
-    for name, t in (("k", new_k), ("v", new_v)):
-        if t.dtype not in _BF16:
-            raise TypeError(f"new_{name} must be bf16, got {t.dtype}")
-        _need(t.dim() == 4 and (t.shape[0], t.shape[2], t.shape[3]) == want and t.stride(3) == 1,
-              f"new_{name} must be [{want[0]}][count][{want[1]}][{want[2]}] with consecutive elements, got "
-              f"{tuple(t.shape)} with strides {t.stride()}")
-        _on(t, kv.device, f"new_{name}")
-        s = t.stride()
-        setattr(n, name, t.data_ptr())
-        setattr(n, name + "_seq", s[0]), setattr(n, name + "_tok", s[1]), setattr(n, name + "_head", s[2])
-    count = int(new_k.shape[1])
-    _need(int(new_v.shape[1]) == count, "new_k and new_v hold different counts of tokens")
-    _ints(new_pos, kv.n_seq, "new_pos", kv.device)
+    shape = new_k.shape
+    if new_k.dtype not in _BF16 or new_v.dtype not in _BF16:
+        raise TypeError(f"new_k and new_v must be bf16, got {new_k.dtype} and {new_v.dtype}")
+    if len(shape) != 4 or new_v.shape != shape or (shape[0], shape[2], shape[3]) != (kv.n_seq, kv.H_kv, kv.d):
+        raise ValueError(f"new_k and new_v must be [{kv.n_seq}][count][{kv.H_kv}][{kv.d}], got {tuple(shape)} and "
+                         f"{tuple(new_v.shape)}")
+    count, device = shape[1], kv.device
+    ks, vs = new_k.stride(), new_v.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError(f"the elements of a row must be consecutive, got strides {ks} and {vs}")
+    if new_k.device != device or new_v.device != device:
+        raise ValueError(f"new_k and new_v are on {new_k.device} and {new_v.device}, expected {device}")
+    _ints(new_pos, kv.n_seq, "new_pos", device)
     if rope_pos is not None:
-        _ints(rope_pos, kv.n_seq * count, "rope_pos", kv.device)
+        _ints(rope_pos, kv.n_seq * count, "rope_pos", device)
     if rope is not None:
-        _on(rope.phases, kv.device, "rope")
-    _call(_lib.misa_append_kv, kv.device, stream, ctypes.byref(kv.struct), ctypes.byref(n), new_pos.data_ptr(), count,
-          None if rope is None else ctypes.byref(rope.struct), _m._ptr(rope_pos), 1 if commit else 0)
+        _on(rope.phases, device, "rope")
+    n = misa_new_kv(new_k.data_ptr(), new_v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    _call(_lib.misa_append_kv, device, stream, kv._p, ctypes.byref(n), new_pos.data_ptr(), count,
+          None if rope is None else rope._p, None if rope_pos is None else rope_pos.data_ptr(), 1 if commit else 0)
 
 
 def read_kv(kv: KVCache, seq: torch.Tensor, tok: torch.Tensor, k_out: Optional[torch.Tensor] = None,
             v_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The dequantised bf16 rows of tokens tok [n][k] (-1: zeros) of sequences seq [n]: two [n][k][H_kv][d] tensors."""
-    _need(tok.dim() == 2, f"tok must be [n][k], got {tuple(tok.shape)}")
-    n, k = (int(x) for x in tok.shape)
-    _ints(seq, n, "seq", kv.device), _ints(tok, n * k, "tok", kv.device)
-    shape = (n, k, kv.H_kv, kv.d)
-    outs = []
+    if tok.dim() != 2:
+        raise ValueError(f"tok must be [n][k], got {tuple(tok.shape)}")
+    n, k = tok.shape
+    device, shape = kv.device, (n, k, kv.H_kv, kv.d)
+    _ints(seq, n, "seq", device), _ints(tok, n * k, "tok", device)
+    if k_out is None or v_out is None:
+        with _allocating(stream):
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=device) if v_out is None else v_out
     for t in (k_out, v_out):
-        if t is None:
-            with _allocating(stream):
-                t = torch.empty(shape, dtype=torch.bfloat16, device=kv.device)
         if t.dtype not in _BF16:
             raise TypeError(f"outputs must be bf16, got {t.dtype}")
-        _need(tuple(t.shape) == shape and t.is_contiguous(), f"outputs must be contiguous {shape}, got {tuple(t.shape)}")
-        _on(t, kv.device, "output")
-        outs.append(t)
-    _call(_lib.misa_read_kv, kv.device, stream, ctypes.byref(kv.struct), seq.data_ptr(), tok.data_ptr(), n, k,
-          outs[0].data_ptr(), outs[1].data_ptr())
-    return outs[0], outs[1]
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"outputs must be contiguous {shape}, got {tuple(t.shape)}")
+        _on(t, device, "output")
+    _call(_lib.misa_read_kv, device, stream, kv._p, seq.data_ptr(), tok.data_ptr(), n, k, k_out.data_ptr(),
+          v_out.data_ptr())
+    return k_out, v_out
 
 
 class AttentionQueries:
@@ -293,6 +307,7 @@ class AttentionQueries:
         self.q, self.q_seq, self.q_pos = q, q_seq, q_pos
         self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(self.d)
         self._s = misa_attend_queries(_m._ptr(q), _m._ptr(q_seq), _m._ptr(q_pos), self.n_q, self.H, self.scale)
+        self._p = ctypes.byref(self._s)
 
     @property
     def struct(self) -> misa_attend_queries:
@@ -312,6 +327,7 @@ class Draft:
         _ints(start, start.numel(), "start", mask.device)
         self.start, self.mask, self.n = start, mask, int(n)
         self._s = misa_draft(_m._ptr(start), _m._ptr(mask), self.n)
+        self._p = ctypes.byref(self._s)
 
     @property
     def struct(self) -> misa_draft:
@@ -347,34 +363,43 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
 
     Returns out [n_q][H][d] (q's type), with ``with_lse`` or a given ``lse`` the pair (out, lse fp32 [n_q][H])."""
     dev = kv.device
-    _need(qs.d == kv.d, f"queries of {qs.d} elements, cache of {kv.d}")
-    _on(qs.q, dev, "q")
-    k = 0
+    if qs.d != kv.d:
+        raise ValueError(f"queries of {qs.d} elements, cache of {kv.d}")
+    q = qs.q
+    _on(q, dev, "q")
+    k = n_draft = 0
     if topk is not None:
-        _need(topk.dim() == 2 and topk.shape[0] == qs.n_q, f"topk must be [{qs.n_q}][k], got {tuple(topk.shape)}")
-        k = int(topk.shape[1])
+        if topk.dim() != 2 or topk.shape[0] != qs.n_q:
+            raise ValueError(f"topk must be [{qs.n_q}][k], got {tuple(topk.shape)}")
+        k = topk.shape[1]
         _ints(topk, qs.n_q * k, "topk", dev)
     if draft is not None:
-        _need(draft.mask.shape[0] == qs.n_q, f"draft mask of {draft.mask.shape[0]} rows for {qs.n_q} queries")
-        _need(draft.start.numel() == kv.n_seq, f"draft start of {draft.start.numel()} for {kv.n_seq} sequences")
+        if draft.mask.shape[0] != qs.n_q or draft.start.numel() != kv.n_seq:
+            raise ValueError(f"draft of {draft.mask.shape[0]} mask rows and {draft.start.numel()} sequences for {qs.n_q} "
+                             f"queries and {kv.n_seq} sequences")
         _on(draft.mask, dev, "draft")
-    kvp, qp = ctypes.byref(kv.struct), ctypes.byref(qs.struct)
-    need = int(_lib.misa_attend_workspace_bytes(kvp, qp, k, 0 if draft is None else draft.n))
+        n_draft = draft.n
+    need = _lib.misa_attend_workspace_bytes(kv._p, qs._p, k, n_draft)
+    buf = None
     with _allocating(stream):
         if out is None:
-            out = torch.empty_like(qs.q)
+            out = torch.empty_like(q)
         if lse is None and with_lse:
-            lse = torch.empty(qs.n_q, qs.H, dtype=torch.float32, device=dev)
-        buf, nb = _m._ws(ws, need, dev)
+            lse = torch.empty((qs.n_q, qs.H), dtype=torch.float32, device=dev)
+        if need:
+            buf = (ws or Workspace(dev)).get(need)
     if out.dtype not in _BF16:
         raise TypeError(f"out must be bf16, got {out.dtype}")
-    _need(out.shape == qs.q.shape and out.is_contiguous(), f"out must be contiguous {tuple(qs.q.shape)}")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
     _on(out, dev, "out")
     if lse is not None:
-        if lse.dtype != torch.float32:
+        if lse.dtype is not torch.float32:
             raise TypeError(f"lse must be float32, got {lse.dtype}")
-        _need(tuple(lse.shape) == (qs.n_q, qs.H) and lse.is_contiguous(), f"lse must be contiguous [{qs.n_q}][{qs.H}]")
+        if lse.shape != (qs.n_q, qs.H) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{qs.n_q}][{qs.H}], got {tuple(lse.shape)}")
         _on(lse, dev, "lse")
-    _call(_lib.misa_attend, dev, stream, kvp, qp, _m._ptr(topk), k,
-          None if draft is None else ctypes.byref(draft.struct), out.data_ptr(), _m._ptr(lse), _m._ptr(buf), nb)
+    _call(_lib.misa_attend, dev, stream, kv._p, qs._p, None if topk is None else topk.data_ptr(), k,
+          None if draft is None else draft._p, out.data_ptr(), None if lse is None else lse.data_ptr(),
+          None if buf is None else buf.data_ptr(), need)
     return out if lse is None else (out, lse)
