@@ -19,9 +19,10 @@
 // turns from accumulator to operand by movmatrix.  The maximum is lazy: while
 // no logit exceeds the reference by 2^8 (base 2) nothing is rescaled and no
 // lane exchanges anything.
-// The warps' (max, sum, O) meet in shared memory at the end; with Z > 1 the
-// CTAs' meet in the workspace, where attend_combine_kernel joins them in a
-// fixed order.
+// The warps' (max, sum, O) meet in shared memory at the end.  Up to 8 shares
+// are the CTAs of a thread-block cluster and join over its distributed shared
+// memory, in a fixed order; more shares meet in the workspace, where
+// attend_combine_kernel joins them.
 //
 // Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
 // bf16 before they meet the values.  e4m3 caches: codes are exact in f16; a
@@ -115,7 +116,8 @@ struct Cfg {
   static constexpr int R = 8 * NR;
   static constexpr int OROW = DH + 8;  // floats between rows of a warp's result
   static constexpr size_t RING = (size_t)NW * STAGES * STAGE;
-  static constexpr size_t JOIN = (size_t)NW * R * (OROW * 4 + 16);
+  // results of the warps, and of the CTA
+  static constexpr size_t JOIN = (size_t)NW * R * (OROW * 4 + 16) + (size_t)R * (DH * 4 + 16);
   static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
 };
 
@@ -233,10 +235,64 @@ __device__ Tile find_tile(const AttendView &a, int per, int want) {
 }
 
 struct Split {
-  float *o;    // [Z][n_q * H][DH]
+  float *o;    // [Z][n_q * H][DH]; nullptr: the Z shares are a cluster
   float4 *ml;  // [Z][n_q * H] (max, sum, reference of O)
   int Z;
 };
+
+// One row's joined parts: base-2 maximum of the logits, sum of the weights
+// relative to it, reference of v.
+struct Part {
+  float M = NEG_INF, Y = NEG_INF, l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+// Join n parts: ml(i) = (max, sum, reference), v(i) = 4 elements of O.
+template <int UNROLL, class ML, class V>
+__device__ __forceinline__ Part join_parts(int n, ML &&ml, V &&v) {
+  Part p;
+#pragma unroll UNROLL
+  for (int i = 0; i < n; ++i) {
+    const float4 m = ml(i);
+    p.M = fmaxf(p.M, m.x);
+    p.Y = fmaxf(p.Y, m.z);
+  }
+  const float ref = p.M == NEG_INF ? 0.f : p.M, yref = p.Y == NEG_INF ? 0.f : p.Y;
+#pragma unroll UNROLL
+  for (int i = 0; i < n; ++i) {
+    const float4 m = ml(i), x = v(i);
+    const float f = ex2(m.z - yref);
+    p.l = fmaf(m.y, ex2(m.x - ref), p.l);
+    p.v.x = fmaf(x.x, f, p.v.x), p.v.y = fmaf(x.y, f, p.v.y), p.v.z = fmaf(x.z, f, p.v.z), p.v.w = fmaf(x.w, f, p.v.w);
+  }
+  return p;
+}
+
+// 4 elements of a finished row, and (d0 == 0) its lse.
+__device__ __forceinline__ void store_row(const AttendView &a, const Part &p, int64_t row, int DH, int d0) {
+  const bool none = p.M == NEG_INF && p.l == 0.f;
+  const float inv = none ? 0.f : ex2((p.Y == NEG_INF ? 0.f : p.Y) - (p.M == NEG_INF ? 0.f : p.M)) / p.l;
+  *reinterpret_cast<uint2 *>(a.out + row * DH + d0) =
+      make_uint2(bf16x2(p.v.x * inv, p.v.y * inv), bf16x2(p.v.z * inv, p.v.w * inv));
+  if (a.lse && d0 == 0) a.lse[row] = none ? NEG_INF : p.M * LN2 + logf(p.l);
+}
+
+// every thread of every CTA of the cluster; shared-memory writes before it are
+// seen by the reads after it
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's p
+__device__ __forceinline__ float4 ld_cluster(const void *p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
 
 // LIST: blockIdx.x = query * row_tiles + tile of its G heads.  Otherwise
 // blockIdx.x = tile of `per` queries * row_tiles + tile of their rows, with
@@ -266,12 +322,31 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     auto row_head = [&](int r) { return hk * G + (per > 1 ? r % G : g0 + r); };
 
     // ---- the tile's tokens: prefix (or list) chunks, then drafted chunks ----
-    int seq, len = 0;
+    int seq = -1, len = 0, cb, ce;
+    int c1 = cdiv(a.k, CH);
     int col_len[NR][2];  // this lane's two columns (rows of the tile) of each n-tile
+    auto divide = [&]() {
+      const int chunks = c1 + (a.draft_start ? cdiv(a.n_draft, CH) : 0), share = cdiv(chunks, Z);
+      cb = min((int)blockIdx.z * share, chunks);
+      ce = min(cb + share, chunks);
+    };
+    // This lane's token (lane & 15) of a chunk as listed, before it is checked
+    // (the list is read ahead of everything else that the kernel waits for).
+    auto listed = [&](int ck) -> int {
+      const int i = ck * CH + (lane & (CH - 1));
+      if (!LIST) return i;
+      return ck < ce && i < a.k ? __ldg(a.topk + (int64_t)t.q0 * a.k + i) : -1;
+    };
+    int tok_q[STAGES];
+    auto read_ahead = [&]() {
+#pragma unroll
+      for (int st = 0; st < STAGES; ++st) tok_q[st] = listed(cb + warp + st * NW);
+    };
     if (LIST) {
+      divide();
+      read_ahead();
       len = attend_prefix(c, a, t.q0, &seq);
     } else {
-      seq = -1;
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -290,13 +365,13 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       len = max(len, __shfl_xor_sync(0xffffffffu, len, 2));
       seq = max(seq, __shfl_xor_sync(0xffffffffu, seq, 1));
       seq = max(seq, __shfl_xor_sync(0xffffffffu, seq, 2));
+      c1 = cdiv(len, CH);
+      divide();
+      read_ahead();
     }
-    const int c1 = seq < 0 ? 0 : cdiv(LIST ? a.k : len, CH);
-    const int chunks = c1 + (seq >= 0 && a.draft_start ? cdiv(a.n_draft, CH) : 0);
-    const int draft0 = seq >= 0 && a.draft_start ? a.draft_start[seq] : 0;
+    const int n_draft = seq >= 0 && a.draft_start ? a.n_draft : 0;  // a query outside the cache sees none
+    const int draft0 = n_draft ? a.draft_start[seq] : 0;
     const int words = cdiv(a.n_draft, 32);
-    const int share = cdiv(chunks, Z);
-    const int cb = min((int)blockIdx.z * share, chunks), ce = min(cb + share, chunks);
 
     // ---- query fragments, the k dimension permuted so that a lane's 16-byte
     // pieces of a key row feed whole A fragments ----
@@ -394,24 +469,15 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     const uint8_t *vb = c.v + (int64_t)max(seq, 0) * c.L_cap * c.H_kv * RB;
     const int64_t sb = (int64_t)max(seq, 0) * c.L_cap * c.H_kv;
 
-    // Row of this lane's token (lane & 15) of a chunk within its sequence's
-    // keys, token * H_kv + head (below 2^25); -1 for none.
-    auto row_of = [&](int ck) -> int {
+    // Row of that token within its sequence's keys, token * H_kv + head (below
+    // 2^25); -1 for none.
+    auto row_of = [&](int ck, int tok) -> int {
       if (ck >= ce) return -1;
-      const int l = lane & (CH - 1);
-      int tok;
       if (ck < c1) {
-        const int i = ck * CH + l;
-        if (LIST) {
-          if (i >= a.k) return -1;
-          tok = __ldg(a.topk + (int64_t)t.q0 * a.k + i);
-        } else {
-          tok = i;
-        }
         if (tok < 0 || tok >= len) return -1;
       } else {
-        const int j = (ck - c1) * CH + l;
-        if (j >= a.n_draft) return -1;
+        const int j = (ck - c1) * CH + (lane & (CH - 1));
+        if (j >= n_draft) return -1;
         if (LIST && !((a.draft_mask[(int64_t)t.q0 * words + (j >> 5)] >> (j & 31)) & 1u)) return -1;
         const int64_t p = (int64_t)draft0 + j;
         if (p < 0 || p >= c.L_cap) {
@@ -462,14 +528,13 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     };
 
     int nxt = cb + warp;
-    int row_n = row_of(nxt);
     uint32_t have_q[STAGES - 1];
 #pragma unroll
     for (int st = 0; st < STAGES - 1; ++st) {
-      have_q[st] = issue(st * F::STAGE, row_n);
+      have_q[st] = issue(st * F::STAGE, row_of(nxt, tok_q[st]));
       nxt += NW;
-      row_n = row_of(nxt);
     }
+    int tok_n = tok_q[STAGES - 1];  // read one turn before it is used
     int at = 0, put_at = (STAGES - 1) * F::STAGE;  // stage read now, stage written now
     for (int ck = cb + warp; ck < ce; ck += NW) {
       cp_async_wait<STAGES - 2>();
@@ -477,9 +542,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       const uint32_t have = have_q[0];
 #pragma unroll
       for (int st = 0; st < STAGES - 2; ++st) have_q[st] = have_q[st + 1];
-      have_q[STAGES - 2] = issue(put_at, row_n);
+      have_q[STAGES - 2] = issue(put_at, row_of(nxt, tok_n));
       nxt += NW;
-      row_n = row_of(nxt);
+      tok_n = listed(nxt);
       uint8_t *sk = ring + at, *sv = sk + CH * RB;
       const float *ss = reinterpret_cast<const float *>(sv + CH * RB);
       put_at = at;
@@ -725,37 +790,33 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         }
       }
     __syncthreads();
+    float *jo = reinterpret_cast<float *>(sml + NW * R);  // [R][DH]: this CTA's share
+    float4 *jml = reinterpret_cast<float4 *>(jo + R * DH);  // [R]
+    const bool in_cluster = Z > 1 && split.o == nullptr;
+    auto out_row = [&](int r) { return (int64_t)row_query(r) * a.H + row_head(r); };
     for (int e = tid; e < n_rows * (DH / 4); e += F::THREADS) {
       const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
-      float M = NEG_INF, Y = NEG_INF;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        M = fmaxf(M, sml[w * R + r].x);
-        Y = fmaxf(Y, sml[w * R + r].z);
-      }
-      const float ref = M == NEG_INF ? 0.f : M, yref = Y == NEG_INF ? 0.f : Y;
-      float l = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float4 ml = sml[w * R + r];
-        const float f = ex2(ml.z - yref);
-        const float4 x = *reinterpret_cast<const float4 *>(so + ((size_t)w * R + r) * F::OROW + d0);
-        l = fmaf(ml.y, ex2(ml.x - ref), l);
-        v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
-      }
-      const int64_t orow = (int64_t)row_query(r) * a.H + row_head(r);
-      if (Z > 1) {
-        const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
-        *reinterpret_cast<float4 *>(split.o + prow * DH + d0) = v;
-        if (d0 == 0) split.ml[prow] = make_float4(M, l, Y, 0.f);
+      const Part p = join_parts<NW>(
+          NW, [&](int w) { return sml[w * R + r]; },
+          [&](int w) { return *reinterpret_cast<const float4 *>(so + ((size_t)w * R + r) * F::OROW + d0); });
+      if (Z == 1) {
+        store_row(a, p, out_row(r), DH, d0);
       } else {
-        const bool none = M == NEG_INF && l == 0.f;
-        const float inv = none ? 0.f : ex2(yref - ref) / l;
-        *reinterpret_cast<uint2 *>(a.out + orow * DH + d0) =
-            make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
-        if (a.lse && d0 == 0) a.lse[orow] = none ? NEG_INF : M * LN2 + logf(l);
+        const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + out_row(r);
+        *reinterpret_cast<float4 *>(in_cluster ? jo + r * DH + d0 : split.o + prow * DH + d0) = p.v;
+        if (d0 == 0) *(in_cluster ? jml + r : split.ml + prow) = make_float4(p.M, p.l, p.Y, 0.f);
       }
+    }
+    if (in_cluster) {
+      // the shares' rows, dealt to the cluster's CTAs (rank = share)
+      cluster_sync();
+      for (int e = blockIdx.z * F::THREADS + tid; e < n_rows * (DH / 4); e += Z * F::THREADS) {
+        const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
+        const Part p = join_parts<8>(
+            Z, [&](int z) { return ld_cluster(jml + r, z); }, [&](int z) { return ld_cluster(jo + r * DH + d0, z); });
+        store_row(a, p, out_row(r), DH, d0);
+      }
+      cluster_sync();  // no CTA overwrites or leaves what another still reads
     }
     if (LIST) break;
     __syncthreads();
@@ -764,43 +825,24 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
   }
 }
 
-// One warp per row: the Z shares' (max, sum, O), joined in order.
+// One block per row: its four quarters join every fourth share, then meet.
 template <int DH>
-__global__ void __launch_bounds__(128) attend_combine_kernel(AttendView a, Split split) {
+__global__ void __launch_bounds__(DH) attend_combine_kernel(AttendView a, Split split) {
   grid_dep_sync();
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n = (int64_t)a.n_q * a.H;
-  const int lane = threadIdx.x & 31;
-  if (row >= n) return;
-  float M = NEG_INF, Y = NEG_INF;
-  for (int z = lane; z < split.Z; z += 32) {
-    const float4 ml = split.ml[z * n + row];
-    M = fmaxf(M, ml.x);
-    Y = fmaxf(Y, ml.z);
-  }
-#pragma unroll
-  for (int x = 16; x; x >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    Y = fmaxf(Y, __shfl_xor_sync(0xffffffffu, Y, x));
-  }
-  const float ref = M == NEG_INF ? 0.f : M, yref = Y == NEG_INF ? 0.f : Y;
-  constexpr int E = DH / 32;
-  float v[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.f;
-  for (int z = 0; z < split.Z; ++z) {
-    const float4 ml = split.ml[z * n + row];
-    const float f = ex2(ml.z - yref);
-    l = fmaf(ml.y, ex2(ml.x - ref), l);
-    const float *p = split.o + (z * n + row) * DH + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(p[e], f, v[e]);
-  }
-  const bool none = M == NEG_INF && l == 0.f;
-  const float inv = none ? 0.f : ex2(yref - ref) / l;
-  uint32_t *out = reinterpret_cast<uint32_t *>(a.out + row * DH + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = bf16x2(v[e] * inv, v[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = none ? NEG_INF : M * LN2 + logf(l);
+  constexpr int LANES = DH / 4;
+  __shared__ float4 ml_s[4], v_s[4][LANES];
+  const int64_t row = blockIdx.x, n = (int64_t)a.n_q * a.H;
+  const int part = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  const Part p = join_parts<4>(
+      (split.Z - part + 3) / 4, [&](int i) { return split.ml[(int64_t)(4 * i + part) * n + row]; },
+      [&](int i) {
+        return *reinterpret_cast<const float4 *>(split.o + ((int64_t)(4 * i + part) * n + row) * DH + 4 * lane);
+      });
+  v_s[part][lane] = p.v;
+  if (lane == 0) ml_s[part] = make_float4(p.M, p.l, p.Y, 0.f);
+  __syncthreads();
+  if (part) return;
+  store_row(a, join_parts<4>(4, [&](int i) { return ml_s[i]; }, [&](int i) { return v_s[i][lane]; }), row, DH, 4 * lane);
 }
 
 struct Plan {
@@ -808,6 +850,7 @@ struct Plan {
   int per;        // queries per tile (1 with lists)
   int row_tiles;  // tiles of a query's G rows (per == 1)
   int tiles, Z;
+  bool cluster;   // the Z shares are a cluster
 };
 
 // Rows of a tile: as many n-tiles as one query's G heads (and, without lists,
@@ -829,9 +872,13 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   const int chunks = cdiv(list ? k : c.L_cap, CH) + cdiv(n_draft, CH);
   const int ctas = ctas_per_sm(c.fp8, c.d, p.nr);
   const int64_t units = (int64_t)tiles * p.row_tiles * c.H_kv;
-  // shares: fill the SMs once, two chunks per warp at the least
+  // shares: fill the SMs once, two chunks per warp at the least.  A cluster of
+  // up to 8 joins them without a second launch; more shares pay off only
+  // where each of 8 would still run through 32 chunks per warp or more.
   const int64_t want = units > 0 ? (int64_t)device_sms() * ctas / units : 1;
   p.Z = (int)std::max<int64_t>(1, std::min<int64_t>(want, chunks / (2 * NW)));
+  if (p.Z > 8 && chunks < 8 * NW * 32) p.Z = 8;
+  p.cluster = p.Z > 1 && p.Z <= 8;
   return p;
 }
 
@@ -840,8 +887,10 @@ cudaError_t run_attend(const KvView &c, const AttendView &a, const Split &sp, co
   struct Tag {};
   const int have = cached_per_device<Tag>([] { return opt_in_max_dyn_smem(attend_kernel<F, LIST>); });
   if (have < (int)F::SMEM) return cudaErrorInvalidConfiguration;
-  return launch_kernel(attend_kernel<F, LIST>, dim3((unsigned)(p.tiles * p.row_tiles), c.H_kv, p.Z), dim3(F::THREADS),
-                       F::SMEM, s, c, a, sp, p.per, p.row_tiles);
+  const dim3 grid((unsigned)(p.tiles * p.row_tiles), c.H_kv, p.Z), block(F::THREADS);
+  return p.cluster ? launch_kernel_cluster(attend_kernel<F, LIST>, grid, block, dim3(1, 1, p.Z), F::SMEM, s, c, a, sp,
+                                           p.per, p.row_tiles)
+                   : launch_kernel(attend_kernel<F, LIST>, grid, block, F::SMEM, s, c, a, sp, p.per, p.row_tiles);
 }
 
 template <int DH, bool FP8, bool LIST>
@@ -862,7 +911,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t attend_ws_bytes(const KvView &c, int n_q, int H, int k, int n_draft) {
   const Plan p = make_plan(c, n_q, H, k, n_draft);
-  if (p.Z <= 1) return 0;
+  if (p.Z <= 1 || p.cluster) return 0;
   const size_t n = (size_t)p.Z * n_q * H;
   return round256(n * c.d * 4) + round256(n * 16);
 }
@@ -871,16 +920,16 @@ cudaError_t launch_attend(const KvView &c, const AttendView &a, void *ws, cudaSt
   if (a.n_q == 0) return cudaSuccess;
   const Plan p = make_plan(c, a.n_q, a.H, a.topk ? a.k : 0, a.n_draft);
   Split sp = {nullptr, nullptr, p.Z};
-  if (p.Z > 1) {
+  if (p.Z > 1 && !p.cluster) {
     sp.o = static_cast<float *>(ws);
     sp.ml = reinterpret_cast<float4 *>(static_cast<uint8_t *>(ws) + round256((size_t)p.Z * a.n_q * a.H * c.d * 4));
   }
   cudaError_t e = c.d == 128 ? (c.fp8 ? pick_attend<128, true>(c, a, sp, p, s) : pick_attend<128, false>(c, a, sp, p, s))
                              : (c.fp8 ? pick_attend<64, true>(c, a, sp, p, s) : pick_attend<64, false>(c, a, sp, p, s));
-  if (e != cudaSuccess || p.Z == 1) return e;
-  const dim3 g((unsigned)(((int64_t)a.n_q * a.H + 3) / 4)), b(128);
-  return c.d == 128 ? launch_kernel(attend_combine_kernel<128>, g, b, 0, s, a, sp)
-                    : launch_kernel(attend_combine_kernel<64>, g, b, 0, s, a, sp);
+  if (e != cudaSuccess || p.Z == 1 || p.cluster) return e;
+  const dim3 g((unsigned)(a.n_q * a.H));
+  return c.d == 128 ? launch_kernel(attend_combine_kernel<128>, g, dim3(128), 0, s, a, sp)
+                    : launch_kernel(attend_combine_kernel<64>, g, dim3(64), 0, s, a, sp);
 }
 
 }  // namespace misa
