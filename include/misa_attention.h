@@ -180,7 +180,7 @@ MISA_API misa_status misa_append_kv(const misa_kv *kv, const misa_new_kv *new_kv
  *   them may be NULL
  * Tokens at and beyond seq_len (drafted ones) are read as they are.
  * Errors: those of the cache; MISA_ERR_INVALID for n < 0, k < 1, NULL seq or
- * tok, or both outputs NULL.
+ * tok, or both outputs NULL; MISA_ERR_UNSUPPORTED for k > MISA_MAX_L.
  */
 MISA_API misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *tok, int32_t n, int32_t k,
                                   uint16_t *k_out, uint16_t *v_out, misa_stream stream);

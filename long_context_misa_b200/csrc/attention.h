@@ -27,6 +27,16 @@ struct RopeView {
   float amplitude;
 };
 
+// Heads that one thread of the rotary and cache kernels takes: `flat` threads
+// would take one each.  A thread's 8 cos and sin cost about 350 instructions,
+// as many as the memory leaves room for per 64 bytes, so a large call shares
+// them over up to 8 heads while half the device's threads remain busy.
+inline int heads_per_thread(int64_t flat, int heads) {
+  int per = 1;
+  while (per < 8 && 2 * per <= heads && flat / (2 * per) >= (int64_t)device_sms() * 1024) per *= 2;
+  return per;
+}
+
 // rope.cu
 cudaError_t launch_rope(const RopeView &r, const misa_rope_rows *groups, int n_groups, cudaStream_t s);
 

@@ -161,6 +161,7 @@ misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *t
   misa_status st = check_kv(kv);
   if (st != MISA_OK) return st;
   if (n < 0 || k < 1) return fail(MISA_ERR_INVALID, "n=%d k=%d", n, k);
+  if (k > MISA_MAX_L) return fail(MISA_ERR_UNSUPPORTED, "k=%d above %d", k, MISA_MAX_L);
   if (!k_out && !v_out) return fail(MISA_ERR_INVALID, "k_out and v_out are both NULL");
   if (n > 0 && (!seq || !tok)) return fail(MISA_ERR_INVALID, "seq/tok is NULL");
   if (!aligned16(k_out) || !aligned16(v_out)) return fail(MISA_ERR_INVALID, "k_out and v_out must be 16-byte aligned");

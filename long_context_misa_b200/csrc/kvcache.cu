@@ -10,6 +10,8 @@
 // of misa_append_keys_e4m3.  The key is rotated in fp32 first and not rounded
 // in between.  A thread keeps its 8 pairs' cos and sin for the heads of a
 // token that it takes one after the other.
+#include <algorithm>
+
 #include "attention.h"
 #include "frag.cuh"
 #include "rope.cuh"
@@ -17,17 +19,47 @@
 namespace misa {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
+
+// Four e4m3 codes of f[0..3] * by (nearest even, saturated), low byte first.
+__device__ __forceinline__ uint32_t codes4(const float *f, float by) {
+  uint32_t c;
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+      : "=r"(c)
+      : "f"(f[0] * by), "f"(f[1] * by), "f"(f[2] * by), "f"(f[3] * by));
+  return c;
+}
+
+// e4m3(f / sc) of 8 elements with the IEEE quotients.  f * inv (inv = 1 / sc to
+// an ulp) is within 2^-21 of the quotient, so where both ends of that interval
+// round to the same code the quotient is not needed.  Otherwise (ties are not
+// rare among bf16 inputs: about one warp in four meets one) the quotient comes
+// from a product in fp64: that is within 2^-52 of it, a quotient of two fp32
+// numbers that is not an fp32 number's midpoint lies at least 2^-49 away from
+// one, and an exact tie is an fp32 number itself, so rounding the product to
+// fp32 gives the IEEE quotient.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float sc, float inv) {
+  const float lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+  const uint2 c = make_uint2(codes4(f, lo), codes4(f + 4, lo));
+  if (((c.x ^ codes4(f, hi)) | (c.y ^ codes4(f + 4, hi))) == 0u && inv <= 0x1p125f) return c;
+  const double r = 1.0 / (double)sc;
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = (float)((double)f[i] * r);
+  return make_uint2(codes4(q, 1.f), codes4(q + 4, 1.f));
+}
 
 // 16 elements (chunks at o1 and o2 of a row) to the cache.  LPR threads hold
 // the row; all 32 lanes call.
-template <int LPR>
-__device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[8], uint8_t *row, float *scale, int o1,
-                                          int o2, bool fp8, bool store, int part) {
-  if (!fp8) {
+template <int LPR, bool FP8>
+__device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[8], uint8_t *cache, float *scales,
+                                          int64_t row, int o1, int o2, bool store, int part) {
+  if (!FP8) {
     if (!store) return;
-    *reinterpret_cast<uint4 *>(row + 2 * o1) = pack8(a);
-    *reinterpret_cast<uint4 *>(row + 2 * o2) = pack8(b);
+    uint16_t *to = reinterpret_cast<uint16_t *>(cache) + row * (LPR * 16);
+    *reinterpret_cast<uint4 *>(to + o1) = pack8(a);
+    *reinterpret_cast<uint4 *>(to + o2) = pack8(b);
     return;
   }
   float m = 0.f;
@@ -36,128 +68,147 @@ __device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!store) return;
-  const float sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
-  uint32_t c[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = f32x2_to_e4m3x2(__fdiv_rn(a[2 * i], sc), __fdiv_rn(a[2 * i + 1], sc)) & 0xFFFFu;
-    c[4 + i] = f32x2_to_e4m3x2(__fdiv_rn(b[2 * i], sc), __fdiv_rn(b[2 * i + 1], sc)) & 0xFFFFu;
+  // m / 448 in IEEE rounding: m / 7 never lies within 2^-29 of an fp32 midpoint
+  // (relatively), far more than the fp64 product is off; denormal quotients
+  // take the division
+  const float sc = m >= 0x1p-100f ? (float)((double)m * (1.0 / 448.0)) : m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+  const float inv = __fdividef(1.f, sc);
+  const uint2 x = codes8(a, sc, inv), y = codes8(b, sc, inv);
+  uint8_t *to = cache + row * (LPR * 16);
+  if (o2 == o1 + 8 && (o1 & 15) == 0) {
+    *reinterpret_cast<uint4 *>(to + o1) = make_uint4(x.x, x.y, y.x, y.y);
+  } else {
+    *reinterpret_cast<uint2 *>(to + o1) = x;
+    *reinterpret_cast<uint2 *>(to + o2) = y;
   }
-  *reinterpret_cast<uint2 *>(row + o1) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  *reinterpret_cast<uint2 *>(row + o2) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
-  if (part == 0) *scale = sc;
+  if (part == 0) scales[row] = sc;
 }
 
-// LPR = d / 16 threads per row.  VEC: the rotated part fits rope_unit's
-// alignment (or nothing is rotated).
-template <int LPR, bool VEC>
-__global__ void __launch_bounds__(THREADS) append_kv_kernel(KvView c, misa_new_kv in, const int32_t *new_pos,
+// LPR = d / 16 threads per row.  ROT: nothing is rotated, or a part that fits
+// rope_unit's alignment, or any part.
+constexpr int ROT_NONE = 0, ROT_VEC = 1, ROT_ANY = 2;
+
+template <int LPR, bool FP8, int ROT>
+__global__ void __launch_bounds__(THREADS, 5) append_kv_kernel(KvView c, misa_new_kv in, const int32_t *new_pos,
                                                             int count, RopeView r, const int32_t *rope_pos,
                                                             int commit, int head_groups) {
   grid_dep_sync();
   constexpr int DH = LPR * 16;
-  const int64_t t = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-  const int part = (int)(t % LPR);
-  int64_t rest = t / LPR;
-  const int hg = (int)(rest % head_groups);
-  rest /= head_groups;
-  const int j = (int)(rest % count);
-  const int64_t s64 = rest / count;
-  const int s = (int)min(s64, (int64_t)c.n_seq - 1);
-  bool live = s64 < c.n_seq;
-  const int pos = new_pos[s];
-  if (pos < 0) live = false;
-  if (live && (int64_t)pos + count > c.L_cap) {
-    if (part == 0 && hg == 0 && j == 0) flag(c, MISA_DEV_APPEND_RANGE);
-    live = false;
-  }
-  if (live && commit && part == 0 && hg == 0 && j == 0) c.seq_len[s] = pos + count;
-  int o1 = 16 * part, o2 = o1 + 8;
-  bool rotated = false;
-  float2 cs[8];
-  int p = 0;
-  if (r.phase) {
-    p = rope_pos ? rope_pos[(int64_t)s * count + j] : pos + j;
-    if (VEC) {
-      rotated = rope_unit(part, DH, r.rot, r.first, r.interleaved, o1, o2);
-      if (rotated) rope_unit_cs(r.phase, part, p, r.amplitude, cs);
+  // blockIdx.x: the (token, head group, part)s of a sequence, below 2^28
+  const uint32_t t = blockIdx.x * THREADS + threadIdx.x, rest = t / LPR;
+  const int part = (int)(t % LPR), j0 = (int)(rest / (uint32_t)head_groups);
+  const int hg = (int)(rest - (uint32_t)j0 * head_groups), j = min(j0, count - 1);
+  for (int s = blockIdx.y; s < c.n_seq; s += gridDim.y) {
+    bool live = j0 < count;
+    const int pos = new_pos[s];
+    if (pos < 0) live = false;
+    if (live && (int64_t)pos + count > c.L_cap) {
+      if (part == 0 && hg == 0 && j == 0) flag(c, MISA_DEV_APPEND_RANGE);
+      live = false;
     }
-  }
-  const uint16_t *k = in.k + s * in.k_seq + j * in.k_tok;
-  const uint16_t *v = in.v + s * in.v_seq + j * in.v_tok;
-  const int esz = c.fp8 ? 1 : 2;
-  const int64_t row0 = ((int64_t)s * c.L_cap + (live ? pos + j : 0)) * c.H_kv;
-  // every lane takes every step: a row's amax is reduced over its lanes
-  for (int h0 = 0; h0 < c.H_kv; h0 += head_groups) {
-    const int h = h0 + hg;
-    const bool store = live && h < c.H_kv;
-    const int hr = store ? h : 0;
-    float a[8], b[8];
-    if (VEC) {
-      unpack8(*reinterpret_cast<const uint4 *>(k + hr * in.k_head + o1), a);
-      unpack8(*reinterpret_cast<const uint4 *>(k + hr * in.k_head + o2), b);
-      if (rotated) rope_unit_rotate(a, b, cs, r.interleaved);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = rope_element(k + hr * in.k_head, o1 + e, r.phase, r.rot, r.first, r.interleaved, p, r.amplitude);
-        b[e] = rope_element(k + hr * in.k_head, o2 + e, r.phase, r.rot, r.first, r.interleaved, p, r.amplitude);
+    if (live && commit && part == 0 && hg == 0 && j == 0) c.seq_len[s] = pos + count;
+    int o1 = 16 * part, o2 = o1 + 8;
+    const bool rotated = ROT == ROT_VEC && rope_unit(part, DH, r.rot, r.first, r.interleaved, o1, o2);
+    const uint16_t *k = in.k + s * in.k_seq + j * in.k_tok;
+    const uint16_t *v = in.v + s * in.v_seq + j * in.v_tok;
+    uint4 raw[4];  // a head's key and value chunks, read one head ahead
+    auto read = [&](int h) {
+      const int hr = h < c.H_kv ? h : 0;
+      if (ROT != ROT_ANY) {
+        raw[0] = *reinterpret_cast<const uint4 *>(k + hr * in.k_head + o1);
+        raw[1] = *reinterpret_cast<const uint4 *>(k + hr * in.k_head + o2);
       }
+      raw[2] = *reinterpret_cast<const uint4 *>(v + hr * in.v_head + o1);
+      raw[3] = *reinterpret_cast<const uint4 *>(v + hr * in.v_head + o2);
+    };
+    read(hg);
+    float2 cs[8];
+    int p = 0;
+    if (ROT != ROT_NONE) p = rope_pos ? rope_pos[(int64_t)s * count + j] : pos + j;
+    if (rotated) rope_unit_cs(r.phase, part, p, r.amplitude, cs);
+    const int64_t row0 = ((int64_t)s * c.L_cap + (live ? pos + j : 0)) * c.H_kv;
+    // every lane takes every step: a row's amax is reduced over its lanes
+    for (int h0 = 0; h0 < c.H_kv; h0 += head_groups) {
+      const int h = h0 + hg;
+      const bool store = live && h < c.H_kv;
+      const int hr = store ? h : 0;
+      float a[8], b[8], va[8], vb[8];
+      if (ROT != ROT_ANY) {
+        unpack8(raw[0], a);
+        unpack8(raw[1], b);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] = rope_element(k + hr * in.k_head, o1 + e, r.phase, r.rot, r.first, r.interleaved, p, r.amplitude);
+          b[e] = rope_element(k + hr * in.k_head, o2 + e, r.phase, r.rot, r.first, r.interleaved, p, r.amplitude);
+        }
+      }
+      unpack8(raw[2], va);
+      unpack8(raw[3], vb);
+      if (h0 + head_groups < c.H_kv) read(h + head_groups);
+      if (rotated) rope_unit_rotate(a, b, cs, r.interleaved);
+      const int64_t row = row0 + hr;
+      store_row<LPR, FP8>(a, b, c.k, c.k_scale, row, o1, o2, store, part);
+      store_row<LPR, FP8>(va, vb, c.v, c.v_scale, row, o1, o2, store, part);
     }
-    float va[8], vb[8];
-    unpack8(*reinterpret_cast<const uint4 *>(v + hr * in.v_head + o1), va);
-    unpack8(*reinterpret_cast<const uint4 *>(v + hr * in.v_head + o2), vb);
-    const int64_t row = row0 + hr;
-    store_row<LPR>(a, b, c.k + row * DH * esz, c.k_scale + (c.fp8 ? row : 0), o1, o2, c.fp8, store, part);
-    store_row<LPR>(va, vb, c.v + row * DH * esz, c.v_scale + (c.fp8 ? row : 0), o1, o2, c.fp8, store, part);
   }
 }
 
-// Thread: 16 elements of one row of the keys or (second half of the grid's y)
-// the values.
-template <int LPR>
-__global__ void __launch_bounds__(THREADS) read_kv_kernel(KvView c, const int32_t *seq, const int32_t *tok,
-                                                          int64_t rows, int k, uint16_t *k_out, uint16_t *v_out) {
+// blockIdx.z: keys or values; blockIdx.y: list; blockIdx.x: the list's
+// pieces of 8 elements, READ_PIECES of them per thread, THREADS apart: a warp
+// stores 512 contiguous bytes at a time.
+constexpr int READ_PIECES = 4;
+
+template <int DH>
+__global__ void __launch_bounds__(THREADS) read_kv_kernel(KvView c, const int32_t *seq, const int32_t *tok, int n,
+                                                          int k, uint16_t *k_out, uint16_t *v_out) {
   grid_dep_sync();
-  constexpr int DH = LPR * 16;
-  const bool keys = k_out && blockIdx.y == 0;
+  constexpr uint32_t PPR = DH / 8;  // pieces per row
+  const bool keys = k_out && blockIdx.z == 0;
   uint16_t *out = keys ? k_out : v_out;
   const uint8_t *src = keys ? c.k : c.v;
   const float *scale = keys ? c.k_scale : c.v_scale;
-  const int64_t t = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-  const int part = (int)(t % LPR);
-  const int64_t orow = t / LPR;  // (i * k + j) * H_kv + h
-  if (orow >= rows) return;
-  const int64_t ij = orow / c.H_kv;
-  const int h = (int)(orow - ij * c.H_kv);
-  const int s = seq[ij / k], token = tok[ij];
-  uint4 *dst = reinterpret_cast<uint4 *>(out + orow * DH) + 2 * part;
-  const bool there = s >= 0 && s < c.n_seq && token >= 0 && token < c.L_cap;
-  if (!there) {
-    if (token != -1 || s < 0 || s >= c.n_seq) flag(c, MISA_DEV_BAD_POSITION);
-    dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const int64_t row = ((int64_t)s * c.L_cap + token) * c.H_kv + h;
-  if (!c.fp8) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(src + row * DH * 2) + 2 * part;
-    const uint4 a = p[0], b = p[1];
-    dst[0] = a;
-    dst[1] = b;
-    return;
-  }
-  const uint4 w = *(reinterpret_cast<const uint4 *>(src + row * DH) + part);
-  const float sc = scale[row];
-  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-  uint32_t o[8];
+  const uint32_t total = (uint32_t)k * c.H_kv * PPR;  // at most 2^29
+  for (int i = blockIdx.y; i < n; i += gridDim.y) {
+    const int s = seq[i];
+    const bool seq_ok = s >= 0 && s < c.n_seq;
+    uint4 v[READ_PIECES];
+    float sc[READ_PIECES];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 lo = e4m3x2_to_f32x2(ww[i] & 0xFFFFu), hi = e4m3x2_to_f32x2(ww[i] >> 16);
-    o[2 * i] = pack_bf16(lo.x * sc, lo.y * sc);
-    o[2 * i + 1] = pack_bf16(hi.x * sc, hi.y * sc);
+    for (int u = 0; u < READ_PIECES; ++u) {
+      const uint32_t e = blockIdx.x * (THREADS * READ_PIECES) + u * THREADS + threadIdx.x;
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      sc[u] = 1.f;
+      if (e >= total) continue;
+      const uint32_t row = e / PPR, j = row / (uint32_t)c.H_kv;
+      const int token = tok[(int64_t)i * k + j];
+      if (!seq_ok || token < 0 || token >= c.L_cap) {
+        if (token != -1 || !seq_ok) flag(c, MISA_DEV_BAD_POSITION);
+        continue;
+      }
+      const int64_t at = ((int64_t)s * c.L_cap + token) * c.H_kv + (row - j * c.H_kv);
+      if (c.fp8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(src + at * DH + (e % PPR) * 8);
+        v[u].x = w.x, v[u].y = w.y;
+        sc[u] = scale[at];
+      } else {
+        v[u] = *reinterpret_cast<const uint4 *>(src + at * DH * 2 + (e % PPR) * 16);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < READ_PIECES; ++u) {
+      const uint32_t e = blockIdx.x * (THREADS * READ_PIECES) + u * THREADS + threadIdx.x;
+      if (e >= total) continue;
+      uint4 o = v[u];
+      if (c.fp8) {
+        const float2 a = e4m3x2_to_f32x2(v[u].x & 0xFFFFu), b = e4m3x2_to_f32x2(v[u].x >> 16);
+        const float2 d = e4m3x2_to_f32x2(v[u].y & 0xFFFFu), f = e4m3x2_to_f32x2(v[u].y >> 16);
+        o = make_uint4(pack_bf16(a.x * sc[u], a.y * sc[u]), pack_bf16(b.x * sc[u], b.y * sc[u]),
+                       pack_bf16(d.x * sc[u], d.y * sc[u]), pack_bf16(f.x * sc[u], f.y * sc[u]));
+      }
+      *reinterpret_cast<uint4 *>(out + ((int64_t)i * total + e) * 8) = o;
+    }
   }
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 }  // namespace
@@ -165,33 +216,36 @@ __global__ void __launch_bounds__(THREADS) read_kv_kernel(KvView c, const int32_
 cudaError_t launch_append_kv(const KvView &c, const misa_new_kv &in, const int32_t *new_pos, int count,
                              const RopeView &r, const int32_t *rope_pos, bool commit, cudaStream_t s) {
   const int lpr = c.d / 16;
-  // heads per thread as in the rotary kernel: several only where the threads
-  // fill the device twice over
-  const int64_t flat = (int64_t)c.n_seq * count * c.H_kv * lpr, full = (int64_t)device_sms() * 4096;
-  int per = 1;
-  while (per < 8 && per < c.H_kv && flat / (2 * per) >= full) per *= 2;
+  // without a rotation there is nothing to share between heads
+  const int per = heads_per_thread((int64_t)c.n_seq * count * c.H_kv * lpr, r.phase ? c.H_kv : 1);
   const int head_groups = cdiv(c.H_kv, per);
-  const int64_t blocks = ((int64_t)c.n_seq * count * head_groups * lpr + THREADS - 1) / THREADS;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const bool vec = !r.phase || (r.rot % 16 == 0 && r.first % 8 == 0);
-  const dim3 g((unsigned)blocks), b(THREADS);
-  const int cm = commit ? 1 : 0;
+  const int blocks = cdiv(count * head_groups * lpr, THREADS);  // below 2^28 threads
+  const int rot = !r.phase ? ROT_NONE : r.rot % 16 == 0 && r.first % 8 == 0 ? ROT_VEC : ROT_ANY;
+  const dim3 g((unsigned)blocks, (unsigned)std::min(c.n_seq, 65535)), b(THREADS);
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, g, b, 0, s, c, in, new_pos, count, r, rope_pos, commit ? 1 : 0, head_groups);
+  };
+  auto by_rot = [&](auto none, auto vec, auto any) {
+    return rot == ROT_NONE ? go(none) : rot == ROT_VEC ? go(vec) : go(any);
+  };
   if (c.d == 128)
-    return vec ? launch_kernel(append_kv_kernel<8, true>, g, b, 0, s, c, in, new_pos, count, r, rope_pos, cm, head_groups)
-               : launch_kernel(append_kv_kernel<8, false>, g, b, 0, s, c, in, new_pos, count, r, rope_pos, cm, head_groups);
-  return vec ? launch_kernel(append_kv_kernel<4, true>, g, b, 0, s, c, in, new_pos, count, r, rope_pos, cm, head_groups)
-             : launch_kernel(append_kv_kernel<4, false>, g, b, 0, s, c, in, new_pos, count, r, rope_pos, cm, head_groups);
+    return c.fp8 ? by_rot(append_kv_kernel<8, true, ROT_NONE>, append_kv_kernel<8, true, ROT_VEC>,
+                          append_kv_kernel<8, true, ROT_ANY>)
+                 : by_rot(append_kv_kernel<8, false, ROT_NONE>, append_kv_kernel<8, false, ROT_VEC>,
+                          append_kv_kernel<8, false, ROT_ANY>);
+  return c.fp8 ? by_rot(append_kv_kernel<4, true, ROT_NONE>, append_kv_kernel<4, true, ROT_VEC>,
+                        append_kv_kernel<4, true, ROT_ANY>)
+               : by_rot(append_kv_kernel<4, false, ROT_NONE>, append_kv_kernel<4, false, ROT_VEC>,
+                        append_kv_kernel<4, false, ROT_ANY>);
 }
 
 cudaError_t launch_read_kv(const KvView &c, const int32_t *seq, const int32_t *tok, int n, int k, uint16_t *k_out,
                            uint16_t *v_out, cudaStream_t s) {
-  const int64_t rows = (int64_t)n * k * c.H_kv;
-  if (rows == 0) return cudaSuccess;
-  const int64_t blocks = (rows * (c.d / 16) + THREADS - 1) / THREADS;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const dim3 g((unsigned)blocks, k_out && v_out ? 2 : 1), b(THREADS);
-  return c.d == 128 ? launch_kernel(read_kv_kernel<8>, g, b, 0, s, c, seq, tok, rows, k, k_out, v_out)
-                    : launch_kernel(read_kv_kernel<4>, g, b, 0, s, c, seq, tok, rows, k, k_out, v_out);
+  if (n == 0) return cudaSuccess;
+  const int blocks = cdiv(k * c.H_kv * (c.d / 8), THREADS * READ_PIECES);  // at most 2^29 pieces
+  const dim3 g((unsigned)blocks, (unsigned)std::min(n, 65535), k_out && v_out ? 2 : 1), b(THREADS);
+  return c.d == 128 ? launch_kernel(read_kv_kernel<128>, g, b, 0, s, c, seq, tok, n, k, k_out, v_out)
+                    : launch_kernel(read_kv_kernel<64>, g, b, 0, s, c, seq, tok, n, k, k_out, v_out);
 }
 
 }  // namespace misa

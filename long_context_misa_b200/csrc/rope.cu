@@ -13,7 +13,7 @@
 namespace misa {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 struct Group {
   const uint16_t *x;
@@ -32,16 +32,25 @@ struct Groups {
   int n;
 };
 
-__global__ void __launch_bounds__(THREADS) rope_kernel(RopeView r, Groups gs) {
+__global__ void __launch_bounds__(THREADS, 6) rope_kernel(RopeView r, Groups gs) {
   grid_dep_sync();
   int w = 0;
   while (w + 1 < gs.n && (int)blockIdx.x >= gs.g[w + 1].block0) ++w;
   const Group &g = gs.g[w];
   const int64_t t = (int64_t)((int)blockIdx.x - g.block0) * THREADS + threadIdx.x;
-  const int u = (int)(t % g.units);
-  const int64_t rest = t / g.units;
-  const int hg = (int)(rest % g.head_groups);
-  const int64_t row = rest / g.head_groups;
+  int u, hg;
+  int64_t row;
+  if (t >> 31) {
+    u = (int)(t % g.units);
+    hg = (int)(t / g.units % g.head_groups);
+    row = t / g.units / g.head_groups;
+  } else {  // (64-bit divisions cost more than the rest of a small row)
+    const uint32_t rest = (uint32_t)t / (uint32_t)g.units;
+    u = (int)((uint32_t)t - rest * g.units);
+    const uint32_t r = rest / (uint32_t)g.head_groups;
+    hg = (int)(rest - r * g.head_groups);
+    row = r;
+  }
   if (row >= g.n) return;
   const int p = g.pos[row];
   const bool in_place = g.x == g.y;
@@ -60,15 +69,32 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(RopeView r, Groups gs) {
       }
       return;
     }
+    // four heads' chunks are on their way while the angles are worked out
+    constexpr int AHEAD = 4;
     float2 cs[8];
-    rope_unit_cs(r.phase, u, p, r.amplitude, cs);
-    for (int h = hg; h < g.H; h += g.head_groups) {
-      float a[8], b[8];
-      unpack8(*reinterpret_cast<const uint4 *>(x + h * g.x_head + o1), a);
-      unpack8(*reinterpret_cast<const uint4 *>(x + h * g.x_head + o2), b);
-      rope_unit_rotate(a, b, cs, r.interleaved);
-      *reinterpret_cast<uint4 *>(y + h * g.y_head + o1) = pack8(a);
-      *reinterpret_cast<uint4 *>(y + h * g.y_head + o2) = pack8(b);
+    bool first = true;
+    for (int h = hg; h < g.H; h += AHEAD * g.head_groups) {
+      uint4 in[AHEAD][2];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int hh = h + i * g.head_groups;
+        if (hh >= g.H) break;
+        in[i][0] = *reinterpret_cast<const uint4 *>(x + hh * g.x_head + o1);
+        in[i][1] = *reinterpret_cast<const uint4 *>(x + hh * g.x_head + o2);
+      }
+      if (first) rope_unit_cs(r.phase, u, p, r.amplitude, cs);
+      first = false;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int hh = h + i * g.head_groups;
+        if (hh >= g.H) break;
+        float a[8], b[8];
+        unpack8(in[i][0], a);
+        unpack8(in[i][1], b);
+        rope_unit_rotate(a, b, cs, r.interleaved);
+        *reinterpret_cast<uint4 *>(y + hh * g.y_head + o1) = pack8(a);
+        *reinterpret_cast<uint4 *>(y + hh * g.y_head + o2) = pack8(b);
+      }
     }
     return;
   }
@@ -106,11 +132,7 @@ cudaError_t launch_rope(const RopeView &r, const misa_rope_rows *groups, int n_g
     g.vec = r.rot % 16 == 0 && r.first % 8 == 0 && q.d % 8 == 0 && on16(q.x) && on16(q.y) && q.x_row % 8 == 0 &&
             q.x_head % 8 == 0 && q.y_row % 8 == 0 && q.y_head % 8 == 0;
     g.units = g.vec ? r.rot / 16 + cdiv(q.d - r.rot, 16) : r.rot / 2 + (q.d - r.rot);
-    // heads per thread: as many as leave two waves of full SMs (2048 threads)
-    // of threads, at most 8
-    const int64_t flat = (int64_t)q.n * g.units * q.H, full = (int64_t)device_sms() * 4096;
-    int per = 1;
-    while (per < 8 && per < q.H && flat / (2 * per) >= full) per *= 2;
+    const int per = heads_per_thread((int64_t)q.n * g.units * q.H, q.H);
     g.head_groups = cdiv(q.H, per);
     g.block0 = (int)blocks;
     blocks += ((int64_t)q.n * g.head_groups * g.units + THREADS - 1) / THREADS;
