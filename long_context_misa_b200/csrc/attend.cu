@@ -11,8 +11,8 @@
 //
 // attend_kernel: a CTA holds up to 8 NR rows of one key/value head and a share
 // of the tokens (blockIdx.z of Z shares).  Each warp runs alone through every
-// NW-th chunk of 16 tokens: it gathers the chunk's rows with 16-byte cp.async
-// into its own ring of three chunks, so no barrier sits in the loop and 100 to
+// NW-th chunk of 16 or 32 tokens: it gathers the chunk's rows with 16-byte cp.async
+// into its own ring of chunks, so no barrier sits in the loop and 100 to
 // 130 KB of rows are in flight per SM.  The tokens are the M side of mma.sync
 // m16n8k16 (S^T = K Q^T, O^T += V^T P^T), the rows the N side: 8 rows pad
 // nothing where M would pad to 16, and a lane keeps two tokens' scales.  P^T
@@ -41,8 +41,10 @@
 namespace misa {
 namespace {
 
-constexpr int CH = 16;  // tokens per chunk
-constexpr uint32_t ALL = (1u << CH) - 1u;
+// Tokens per chunk: two m-tiles of e4m3 rows (their widening makes the loop
+// bound by instructions, and a longer chunk shares its bookkeeping), one of
+// bf16 rows, whose rings take twice the memory, and beside the O of 32 rows.
+__host__ __device__ constexpr int chunk_tokens(bool fp8, int nr) { return fp8 && nr == 2 ? 32 : 16; }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -58,21 +60,31 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
+// base + x * BYTES in one instruction
+template <int BYTES>
+__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t x) {
+  uint64_t p;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(x), "n"(BYTES), "l"(base));
+  return reinterpret_cast<const uint8_t *>(p);
+}
+
 // Warps per CTA, CTAs per SM and chunks in a warp's ring: as many warps as the
 // registers of their O (32 per n-tile and d = 128) allow, their rings sharing
 // the SM's shared memory.
 constexpr int NW = 4;
 __host__ __device__ constexpr int ctas_per_sm(bool fp8, int d, int nr) {
-  return nr > 2 ? 2 : fp8 ? (nr > 1 && d > 64 ? 3 : 4) : d > 64 ? 2 : 4;
+  return nr > 2 ? 2 : fp8 ? (nr > 1 ? (d > 64 ? 2 : 3) : 4) : d > 64 ? 2 : 4;
 }
 __host__ __device__ constexpr int ring_chunks(bool fp8, int d, int nr) {
-  return fp8 && d > 64 ? (nr > 2 ? 6 : nr > 1 ? 4 : 3) : fp8 || d == 64 ? (nr > 2 ? 4 : 3) : 3;
+  return nr > 2 ? (fp8 ? 6 : d > 64 ? 3 : 4) : 3;
 }
 
 template <int DH_, bool FP8_, int NR_>
 struct Cfg {
   static constexpr int DH = DH_, NR = NR_;
   static constexpr bool FP8 = FP8_;
+  static constexpr int CH = chunk_tokens(FP8, NR), MTL = CH / 16;  // tokens of a chunk, their m-tiles
+  static constexpr uint32_t ALL = 0xffffffffu >> (32 - CH);
   static constexpr int RB = DH * (FP8 ? 1 : 2);  // bytes per row
   static constexpr int CPR = RB / 16;            // 16-byte pieces per row
   static constexpr int KT = DH / 16;             // k-tiles of S, m-tiles of O
@@ -106,7 +118,9 @@ template <class F, bool LIST>
 __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     attend_kernel(KvView c, AttendView a, Split split, int per, int row_tiles) {
   grid_dep_sync();
-  constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT;
+  constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT, CH = F::CH,
+                MTL = F::MTL;
+  constexpr uint32_t ALL = F::ALL;
   constexpr bool FP8 = F::FP8;
   constexpr int STAGES = F::STAGES;
   constexpr bool Q_SMEM = NR > (FP8 ? 1 : 2);  // the query fragments do not fit beside O
@@ -135,7 +149,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       cb = min((int)blockIdx.z * share, chunks);
       ce = min(cb + share, chunks);
     };
-    // This lane's token (lane & 15) of a chunk as listed, before it is checked
+    // This lane's token (lane & (CH - 1)) of a chunk as listed, before it is checked
     // (the list is read ahead of everything else that the kernel waits for).
     auto listed = [&](int ck) -> int {
       const int i = ck * CH + (lane & (CH - 1));
@@ -306,10 +320,10 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       auto copy = [&](auto &&put) {
 #pragma unroll
         for (int it = 0; it < CH / RPI; ++it) {
-          const int x = __shfl_sync(0xffffffffu, max(row, 0), it * RPI + q0r);
-          const uint64_t off = (uint64_t)(uint32_t)x * RB;
+          const uint32_t x = __shfl_sync(0xffffffffu, (uint32_t)max(row, 0), it * RPI + q0r);
           // (the bits of it * RPI and of q0r do not meet)
-          put(it, dk + at + it * RPI * RB, kl + off, dv + at + it * RPI * RB + (v0 ^ v_piece<RB>(it * RPI, 0) * 16), vl + off);
+          put(it, dk + at + it * RPI * RB, row_at<RB>(kl, x),
+              dv + at + it * RPI * RB + (v0 ^ v_piece<RB>(it * RPI, 0) * 16), row_at<RB>(vl, x));
         }
       };
       static_assert(RPI % 2 == 0, "k_piece's row parity");
@@ -325,9 +339,10 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           cp_async16(va, vs, there);
         });
       }
-      if (FP8 && have)
-        cp_async4(ring_a + at + 2 * CH * RB + lane * 4, (lane < CH ? c.k_scale : c.v_scale) + sb + max(row, 0),
-                  row >= 0);
+      if (FP8 && have && lane < CH) {
+        cp_async4(ring_a + at + 2 * CH * RB + lane * 4, c.k_scale + sb + max(row, 0), row >= 0);
+        cp_async4(ring_a + at + 2 * CH * RB + (CH + lane) * 4, c.v_scale + sb + max(row, 0), row >= 0);
+      }
       cp_async_commit();
       return have;
     };
@@ -357,37 +372,46 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       if (!have) continue;
 
       // ---- S^T = K Q^T ----
-      float s[NR][4];
+      float s[NR][MTL][4];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int m = 0; m < MTL; ++m) s[n][m][0] = s[n][m][1] = s[n][m][2] = s[n][m][3] = 0.f;
 #pragma unroll
       for (int ch = 0; ch < RB / 64; ++ch) {
-        const uint4 A = *reinterpret_cast<const uint4 *>(sk + g * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
-        const uint4 B = *reinterpret_cast<const uint4 *>(sk + (g + 8) * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
-        const uint32_t wa[4] = {A.x, A.y, A.z, A.w}, wb[4] = {B.x, B.y, B.z, B.w};
+        uint4 A[MTL], B[MTL], q4 = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int m = 0; m < MTL; ++m) {
+          A[m] = *reinterpret_cast<const uint4 *>(sk + (16 * m + g) * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
+          B[m] = *reinterpret_cast<const uint4 *>(sk + (16 * m + g + 8) * RB + k_piece<RB>(g, 4 * ch + c4) * 16);
+        }
 #pragma unroll
         for (int u = 0; u < (FP8 ? 4 : 2); ++u) {
           const int kt = ch * (FP8 ? 4 : 2) + u;
-          uint32_t af[4];
-          if (FP8) {
-            widen(wa[u], af[0], af[2]);
-            widen(wb[u], af[1], af[3]);
-          } else {
-            af[0] = wa[2 * u], af[1] = wb[2 * u], af[2] = wa[2 * u + 1], af[3] = wb[2 * u + 1];
+          uint32_t af[MTL][4];
+#pragma unroll
+          for (int m = 0; m < MTL; ++m) {
+            const uint32_t wa[4] = {A[m].x, A[m].y, A[m].z, A[m].w}, wb[4] = {B[m].x, B[m].y, B[m].z, B[m].w};
+            if (FP8) {
+              widen(wa[u], af[m][0], af[m][2]);
+              widen(wb[u], af[m][1], af[m][3]);
+            } else {
+              af[m][0] = wa[2 * (u & 1)], af[m][1] = wb[2 * (u & 1)];
+              af[m][2] = wa[2 * (u & 1) + 1], af[m][3] = wb[2 * (u & 1) + 1];
+            }
           }
-          if (Q_SMEM) {
 #pragma unroll
-            for (int n = 0; n < NR; n += 2) {
-              const uint4 q = *reinterpret_cast<const uint4 *>(q_s + ((kt * (NR / 2) + n / 2) * 32 + lane) * 2);
-              FP8 ? mma_f16_16816(s[n], af, q.x, q.y) : mma_bf16_16816(s[n], af, q.x, q.y);
-              FP8 ? mma_f16_16816(s[n + 1], af, q.z, q.w) : mma_bf16_16816(s[n + 1], af, q.z, q.w);
+          for (int n = 0; n < NR; ++n) {
+            uint2 q;
+            if (Q_SMEM) {
+              if ((n & 1) == 0) q4 = *reinterpret_cast<const uint4 *>(q_s + ((kt * (NR / 2) + n / 2) * 32 + lane) * 2);
+              q = n & 1 ? make_uint2(q4.z, q4.w) : make_uint2(q4.x, q4.y);
+            } else {
+              q = qf[Q_SMEM ? 0 : kt][Q_SMEM ? 0 : n];
             }
-          } else {
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-              const uint2 q = qf[Q_SMEM ? 0 : kt][Q_SMEM ? 0 : n];
-              FP8 ? mma_f16_16816(s[n], af, q.x, q.y) : mma_bf16_16816(s[n], af, q.x, q.y);
-            }
+            for (int m = 0; m < MTL; ++m)
+              FP8 ? mma_f16_16816(s[n][m], af[m], q.x, q.y) : mma_bf16_16816(s[n][m], af[m], q.x, q.y);
           }
         }
       }
@@ -423,14 +447,14 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         masked |= mixed;
       }
 
-      // ---- weights of the tokens g and g + 8 (index y) for the columns x:
-      // p = e^(s - ref) for the sum, w for the values ----
-      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+      // ---- weights of the tokens g + 8 y for the columns x: p = e^(s - ref)
+      // for the sum, w for the values ----
+      float ks[2 * MTL], vs[2 * MTL];
       if (FP8) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) ks[y] = ss[g + 8 * y], vs[y] = ss[CH + g + 8 * y];
+        for (int y = 0; y < 2 * MTL; ++y) ks[y] = ss[g + 8 * y], vs[y] = ss[CH + g + 8 * y];
       }
-      float p[NR][4], w[NR][4];
+      float p[NR][4 * MTL], w[NR][4 * MTL];
       auto logit = [&](auto m, float v, int n, int x, int y) {
         return m.value && !(((LIST ? have : vis[n][x]) >> (g + 8 * y)) & 1u) ? NEG_INF : v;
       };
@@ -441,9 +465,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < 2 * MTL; ++y) {
               const int e = 2 * y + x;
-              const float v = logit(m, fmaf(s[n][e], FP8 ? ks[y] * mul[n][x] : mul[n][x], -m_ref[n][x]), n, x, y);
+              const float v = logit(m, fmaf(s[n][y >> 1][e & 3], FP8 ? ks[y] * mul[n][x] : mul[n][x], -m_ref[n][x]), n, x, y);
               p[n][e] = ex2(v);
               w[n][e] = p[n][e];
               if (FP8) {
@@ -465,8 +489,8 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           for (int x = 0; x < 2; ++x) {
             float mx = NEG_INF, my = NEG_INF;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float v = logit(std::true_type(), s[n][2 * y + x] * (FP8 ? ks[y] * mul[n][x] : mul[n][x]), n, x, y);
+            for (int y = 0; y < 2 * MTL; ++y) {
+              const float v = logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * (FP8 ? ks[y] * mul[n][x] : mul[n][x]), n, x, y);
               mx = fmaxf(mx, v);
               if (FP8) my = fmaxf(my, v + __log2f(vs[y] < 0x1p-100f ? 0x1p-100f : vs[y]));  // a NaN stays
             }
@@ -487,15 +511,15 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
             fac[n][x] = m_new == NEG_INF || !FP8 ? 1.f : ex2(m_new - y_new);
           }
       }
-      uint32_t pb[NR][2];
+      uint32_t pb[NR][2 * MTL];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) l_sum[n][x] += p[n][x] + p[n][2 + x];
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2 * MTL; ++y) {
+          l_sum[n][0] += p[n][2 * y];
+          l_sum[n][1] += p[n][2 * y + 1];
           pb[n][y] = movmatrix_trans(FP8 ? f16x2(w[n][2 * y], w[n][2 * y + 1]) : bf16x2(w[n][2 * y], w[n][2 * y + 1]));
-      }
+        }
 
       // ---- values that some rows must not see: a NaN or infinity there would
       // reach them as 0 * NaN.  Such values are taken out of the chunk and
@@ -523,7 +547,11 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
               for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const float wt = __shfl_sync(0xffffffffu, r < 8 ? w[n][x] : w[n][2 + x], (r & 7) * 4 + c4);
+                  float wt = w[n][x];  // token r's weight sits with the lanes of row r % 8
+#pragma unroll
+                  for (int y = 1; y < 2 * MTL; ++y)
+                    if (y == r >> 3) wt = w[n][2 * y + x];
+                  wt = __shfl_sync(0xffffffffu, wt, (r & 7) * 4 + c4);
                   if (g != gt || !((vis[n][x] >> r) & 1u)) continue;
 #pragma unroll
                   for (int j = 0; j < KT; ++j)
@@ -548,23 +576,26 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       const uint32_t sva = smem_addr(sv);
 #pragma unroll
       for (int j = 0; j < CPR / 2; ++j) {
-        uint32_t r[4];
-        const int vr = (FP8 ? mi & 1 : mi >> 1) * 8 + (lane & 7), pc = 2 * j + (FP8 ? mi >> 1 : mi & 1);
-        ldmatrix_x4_trans(r, sva + vr * RB + v_piece<RB>(vr, pc) * 16);
-        if (FP8) {
-          // a register holds elements (2g, 2g + 1) of tokens 2c and 2c + 1:
-          // the even elements are rows 0..7 of an m-tile, the odd ones 8..15
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t af[4];
-            widen(__byte_perm(r[2 * h], 0, 0x3120), af[0], af[1]);
-            widen(__byte_perm(r[2 * h + 1], 0, 0x3120), af[2], af[3]);
+        for (int m = 0; m < MTL; ++m) {
+          uint32_t r[4];
+          const int vr = 16 * m + (FP8 ? mi & 1 : mi >> 1) * 8 + (lane & 7), pc = 2 * j + (FP8 ? mi >> 1 : mi & 1);
+          ldmatrix_x4_trans(r, sva + vr * RB + v_piece<RB>(vr, pc) * 16);
+          if (FP8) {
+            // a register holds elements (2g, 2g + 1) of tokens 2c and 2c + 1:
+            // the even elements are rows 0..7 of an m-tile, the odd ones 8..15
 #pragma unroll
-            for (int n = 0; n < NR; ++n) mma_f16_16816(o[2 * j + h][n], af, pb[n][0], pb[n][1]);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t af[4];
+              widen(__byte_perm(r[2 * h], 0, 0x3120), af[0], af[1]);
+              widen(__byte_perm(r[2 * h + 1], 0, 0x3120), af[2], af[3]);
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_f16_16816(o[2 * j + h][n], af, pb[n][2 * m], pb[n][2 * m + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma_bf16_16816(o[j][n], r, pb[n][2 * m], pb[n][2 * m + 1]);
           }
-        } else {
-#pragma unroll
-          for (int n = 0; n < NR; ++n) mma_bf16_16816(o[j][n], r, pb[n][0], pb[n][1]);
         }
       }
     }
@@ -693,7 +724,7 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   p.row_tiles = p.per > 1 ? 1 : cdiv(G, R);
   p.tiles = list ? n_q : std::min(n_q, cdiv(n_q, p.per) + seqs);
   const int tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
-  const int chunks = cdiv(list ? k : c.L_cap, CH) + cdiv(n_draft, CH);
+  const int ch = chunk_tokens(c.fp8, p.nr), chunks = cdiv(list ? k : c.L_cap, ch) + cdiv(n_draft, ch);
   const int ctas = ctas_per_sm(c.fp8, c.d, p.nr);
   const int64_t units = (int64_t)tiles * p.row_tiles * c.H_kv;
   // shares: fill the SMs once, two chunks per warp at the least.  A cluster of

@@ -32,7 +32,7 @@ struct Groups {
   int n;
 };
 
-__global__ void __launch_bounds__(THREADS, 6) rope_kernel(RopeView r, Groups gs) {
+__global__ void __launch_bounds__(THREADS, 5) rope_kernel(RopeView r, Groups gs) {
   grid_dep_sync();
   int w = 0;
   while (w + 1 < gs.n && (int)blockIdx.x >= gs.g[w + 1].block0) ++w;
