@@ -282,8 +282,10 @@ def read_kv(kv: KVCache, seq: torch.Tensor, tok: torch.Tensor, k_out: Optional[t
     _ints(seq, n, "seq", device), _ints(tok, n * k, "tok", device)
     if k_out is None or v_out is None:
         with _allocating(stream):
-            k_out = torch.empty(shape, dtype=torch.bfloat16, device=device) if k_out is None else k_out
-            v_out = torch.empty(shape, dtype=torch.bfloat16, device=device) if v_out is None else v_out
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+            if v_out is None:
+                v_out = torch.empty_like(k_out)
     for t in (k_out, v_out):
         if t.dtype not in _BF16:
             raise TypeError(f"outputs must be bf16, got {t.dtype}")
@@ -306,6 +308,8 @@ class AttentionQueries:
         _ints(q_seq, self.n_q, "q_seq", q.device), _ints(q_pos, self.n_q, "q_pos", q.device)
         self.q, self.q_seq, self.q_pos = q, q_seq, q_pos
         self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(self.d)
+        # one element in the shape of an lse: torch allocates like a tensor in half the time of a new one
+        self._lse = torch.empty((1, 1), dtype=torch.float32, device=q.device).expand(self.n_q, self.H)
         self._s = misa_attend_queries(_m._ptr(q), _m._ptr(q_seq), _m._ptr(q_pos), self.n_q, self.H, self.scale)
         self._p = ctypes.byref(self._s)
 
@@ -385,7 +389,7 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
         if out is None:
             out = torch.empty_like(q)
         if lse is None and with_lse:
-            lse = torch.empty((qs.n_q, qs.H), dtype=torch.float32, device=dev)
+            lse = torch.empty_like(qs._lse, memory_format=torch.contiguous_format)
         if need:
             buf = (ws or Workspace(dev)).get(need)
     if out.dtype not in _BF16:

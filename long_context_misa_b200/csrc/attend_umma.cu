@@ -4,19 +4,21 @@
 // numbers as attend.cu.
 //
 // A CTA holds up to 128 rows (lanes of tensor memory) of one key/value head
-// and a share of the tokens, in chunks of 128:
+// and a share of the tokens, in chunks of 64:
 //   8 producer warps   gather a chunk's keys (4 warps) and values (4) into
 //                      rings of 128-byte-swizzled tiles: cp.async for bf16
-//                      rows; e4m3 rows are loaded one chunk ahead into
-//                      registers and widened to f16 on their way
+//                      rows; e4m3 rows go through a ring of their own and are
+//                      widened to f16 by the threads that brought them
 //   1 MMA thread       S_j = Q K_j^T and O += P_j V_j (V as the MN-major
 //                      operand, P from tensor memory), S_(j+1) before P_j V_j
 //   4 softmax warps    one row per thread: S from tensor memory, weights back
 //                      into it, the running sum; O is touched only when a
 //                      weight passes 256 times its reference
-// Tensor memory: O [0, 128), two S of 128 columns, two P of 64.  A tile of
-// 128 tokens (64 KB bf16) costs 1024 cycles of MMA at M = 128 and about 1100
-// of softmax issue beside them, against 2850 cycles of its share of HBM.
+// Tensor memory: O [0, 128), two S of 64 columns, two P of 32.  A tile of 64
+// tokens (32 KB bf16) costs 512 cycles of MMA at M = 128 and about 550 of
+// softmax issue beside them, against 1425 cycles of its share of HBM.  Tiles
+// of 64 tokens keep less of the rings waiting than tiles of 128 (measured:
+// see TOK).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -25,11 +27,12 @@
 namespace misa {
 namespace {
 
-constexpr int M = 128, TOK = 128;  // rows and tokens of a tile
+constexpr int M = 128, TOK = 64;  // rows and tokens of a tile
+constexpr int W = TOK / 32;        // mask words of a tile
 constexpr int WARPS = 13, THREADS = WARPS * 32;
 constexpr int PROD0 = 4, MMA_WARP = 12;  // warps 4..7 keys, 8..11 values
-constexpr int SLOTS = 8;                 // scales and masks in flight (more than any ring can be ahead)
-constexpr int T_O = 0, T_S = 128, T_P = 384, T_COLS = 512;
+constexpr int SLOTS = 32;                // masks and scales in flight (more than the rings can be ahead)
+constexpr int T_O = 0, T_S = 128, T_P = 256, T_COLS = 512;
 constexpr int BAD = 256;  // non-finite values handled per round
 
 template <int DH_, bool FP8_>
@@ -38,25 +41,35 @@ struct UCfg {
   static constexpr bool FP8 = FP8_;
   static constexpr int TILE = TOK * DH * 2;  // one operand tile in shared memory, 16-bit elements
   static constexpr int BLK = TOK * 128;      // its blocks of 64 elements
-  static constexpr int NK = DH > 64 ? 2 : 5, NV = DH > 64 ? 3 : 6;  // ring stages
+  static constexpr int QBLK = M * 128, QTILE = M * DH * 2;
   static constexpr int CPR = DH * (FP8 ? 1 : 2) / 16;  // 16-byte pieces of a row as stored
-  static constexpr int SMEM = (1 + NK + NV) * TILE + 1024;
+  static constexpr int PER = TOK * CPR / 128;          // of them per producer thread and tile
+  static constexpr int RAW = FP8 ? TOK * DH : 0;       // a tile of codes
+  // ring stages: operand tiles of keys and values, tiles of codes of either
+  static constexpr int NK = FP8 ? 2 : DH > 64 ? 4 : 8, NV = FP8 ? 3 : DH > 64 ? 6 : 10, NR = FP8 ? (DH > 64 ? 5 : 8) : 0;
+  static constexpr int SMEM = QTILE + (NK + NV) * TILE + 2 * NR * RAW + 1024;
+  static_assert(NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
 };
+constexpr int MAX_STAGES = 10;
 
 struct Shared {
-  uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
+  uint64_t kfull[MAX_STAGES], kempty[MAX_STAGES], vfull[MAX_STAGES], vempty[MAX_STAGES];
   uint64_t sfull[2], sfree[2], pfull[2], pvdone[2], done;
   uint64_t placed[2], scan;  // meetings of a producer group, of the softmax warps
   uint32_t tmem_base;
   int abort;
-  int row_idx[2][2][TOK];    // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
-  uint32_t have[SLOTS][4];   // which tokens of a chunk are there
-  alignas(16) float ks[SLOTS][TOK], vs[SLOTS][TOK];  // read four at a time
+  int row_idx[2][2][TOK];   // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
+  uint32_t have[SLOTS][W];  // which tokens of a chunk are there
   int len[M], query[M];
   int seq, max_len, min_len;
   int n_bad;
-  int2 bad_at[BAD];          // (token, element)
+  int2 bad_at[BAD];  // (token, element)
   float bad_val[BAD];
+};
+
+template <bool FP8>
+struct Scales {
+  alignas(16) float k[FP8 ? SLOTS : 1][TOK], v[FP8 ? SLOTS : 1][TOK];  // read four at a time
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, const KvView &c) {
@@ -105,17 +118,9 @@ __device__ __forceinline__ void st1(uint32_t t, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(v) : "memory");
 }
 
-// whether phase `parity` of `bar` is complete, without waiting
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// arrive on `bar` once this thread's copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ void mbar_inval(uint64_t *bar) {
@@ -131,13 +136,14 @@ __device__ __forceinline__ uint32_t tile_at(int r, int pc, int blk) {
 template <class F, bool LIST>
 __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, AttendView a, Split split, int per) {
   grid_dep_sync();
-  constexpr int DH = F::DH, NK = F::NK, NV = F::NV, BLK = F::BLK, TILE = F::TILE, CPR = F::CPR;
+  constexpr int DH = F::DH, NK = F::NK, NV = F::NV, BLK = F::BLK, TILE = F::TILE, CPR = F::CPR, PER = F::PER;
   constexpr bool FP8 = F::FP8;
   extern __shared__ uint8_t raw_smem[];
   __shared__ Shared sh;
+  __shared__ Scales<FP8> scales;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t *smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
-  uint8_t *q_s = smem, *k_s = smem + TILE, *v_s = k_s + NK * TILE;
+  uint8_t *q_s = smem, *k_s = smem + F::QTILE, *v_s = k_s + NK * TILE, *raw_s = v_s + NV * TILE;
   const int G = a.H / c.H_kv, hk = blockIdx.y, Z = split.Z;
   volatile int *abort = &sh.abort;
 
@@ -160,8 +166,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
     auto row_head = [&](int r) { return hk * G + r % G; };
     // ---- barriers, rows ----
     if (tid == 0) {
-      for (int i = 0; i < 6; ++i) {
-        mbar_init(&sh.kfull[i], 128), mbar_init(&sh.vfull[i], 128);  // every producer thread of the group
+      for (int i = 0; i < MAX_STAGES; ++i) {
+        // every producer thread of the group (bf16: as its copies land, and
+        // the lanes that noted the masks)
+        mbar_init(&sh.kfull[i], 128), mbar_init(&sh.vfull[i], FP8 ? 128 : 128 + W);
         mbar_init(&sh.kempty[i], 1), mbar_init(&sh.vempty[i], 1);    // the MMAs' commit
       }
       for (int i = 0; i < 2; ++i) {
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           }
           v = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(q_s + tile_at(tid, p, BLK)) = v;
+        *reinterpret_cast<uint4 *>(q_s + tile_at(tid, p, F::QBLK)) = v;
       }
     }
     umma::fence_proxy_async();
@@ -242,14 +250,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
     if (warp >= PROD0 && warp < MMA_WARP) {
       // ---- producers ----
       const bool vals = warp >= PROD0 + 4;
-      const int pt = (tid - PROD0 * 32) & 127;
+      const int pt = (tid - PROD0 * 32) & 127, lt = pt & (TOK - 1);  // (threads beyond TOK repeat the first ones' tokens)
       uint64_t *full = vals ? sh.vfull : sh.kfull, *empty = vals ? sh.vempty : sh.kempty;
       const uint8_t *base = (vals ? c.v : c.k) + (int64_t)max(seq, 0) * c.L_cap * c.H_kv * (CPR * 16);
       const int64_t srow = (int64_t)max(seq, 0) * c.L_cap * c.H_kv;
       uint8_t *ring = vals ? v_s : k_s;
       const int nst = vals ? NV : NK;
-      auto listed = [&](int j) -> int {  // token pt of chunk j as listed
-        const int i = (cb + j) * TOK + pt;
+      auto listed = [&](int j) -> int {  // token lt of chunk j as listed
+        const int i = (cb + j) * TOK + lt;
         if (!LIST) return i;
         return j < n && i < a.k ? __ldg(a.topk + (int64_t)t.q0 * a.k + i) : -1;
       };
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         if (cb + j < c1) {
           if (tok < 0 || tok >= max_len) return -1;
         } else {
-          const int d = (cb + j - c1) * TOK + pt;
+          const int d = (cb + j - c1) * TOK + lt;
           if (d >= n_draft) return -1;
           if (LIST && !((a.draft_mask[(int64_t)t.q0 * words + (d >> 5)] >> (d & 31)) & 1u)) return -1;
           const int64_t p = (int64_t)draft0 + d;
@@ -273,97 +281,113 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       // rows of chunk j into row_idx[..][j & 1]; the values' group also notes
       // which are there and (e4m3) brings the scales, for the softmax warps,
       // who wait for the values' tile
-      auto place = [&](int j, int row) -> bool {
-        sh.row_idx[vals][j & 1][pt] = row;
-        if (vals) {
-          const uint32_t b = __ballot_sync(0xffffffffu, row >= 0);
-          if (lane == 0 && j < n) sh.have[j & (SLOTS - 1)][pt >> 5] = b;
-        }
-        mbar_arrive(&sh.placed[vals]);
-        return wait_bar(&sh.placed[vals], j & 1, abort, c);
+      const bool notes = vals && pt < TOK && lane == 0;
+      int meetings = 0;
+      auto bring_scale = [&](int j, int row) {
+        float(*to)[TOK] = pt < TOK ? scales.k : scales.v;
+        cp_async4(smem_addr(&to[j & (SLOTS - 1)][lt]), (pt < TOK ? c.k_scale : c.v_scale) + srow + max(row, 0), row >= 0);
       };
-      constexpr int PER = CPR;  // pieces per thread: 128 rows x CPR over 128 threads
+      auto place = [&](int j, int row) -> bool {
+        if (!LIST && cb + j < c1) {
+          const int left = max_len - (cb + j) * TOK - pt;  // (pt is 0 or 32 where it notes)
+          if (notes) sh.have[j & (SLOTS - 1)][pt >> 5] = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+          if (FP8 && vals) bring_scale(j, row);
+          return true;
+        }
+        if (pt < TOK) sh.row_idx[vals][j & 1][pt] = row;
+        const uint32_t b = __ballot_sync(0xffffffffu, row >= 0);
+        if (notes) sh.have[j & (SLOTS - 1)][pt >> 5] = b;
+        if (FP8 && vals) bring_scale(j, row);
+        mbar_arrive(&sh.placed[vals]);
+        return wait_bar(&sh.placed[vals], meetings++ & 1, abort, c);
+      };
       const int pc = pt % CPR, r0 = pt / CPR;
       constexpr int RSTEP = 128 / CPR;
-      int j = 0;
+      // whether chunk j is a stretch of the prefix: its rows need no list, and
+      // no meeting of the group to share one
+      auto stretch = [&](int j) { return !LIST && cb + j < c1; };
+      const uint8_t *lane0 = base + ((int64_t)r0 * c.H_kv + hk) * (CPR * 16) + pc * 16;
+      const int64_t step = (int64_t)RSTEP * c.H_kv * (CPR * 16);
+      // this thread's pieces of chunk j: rows r0, r0 + RSTEP, ... to at(i, row)
+      auto copy = [&](int j, auto &&at) {
+        if (stretch(j)) {
+          const int t0 = (cb + j) * TOK, left = max_len - t0;
+          const uint8_t *p = lane0 + (int64_t)t0 * c.H_kv * (CPR * 16);
+          if (left >= TOK) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i, p += step) cp_async16(at(i, r0 + i * RSTEP), p);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i, p += step) {
+              const bool there = r0 + i * RSTEP < left;
+              cp_async16(at(i, r0 + i * RSTEP), there ? p : base, there);
+            }
+          }
+          return;
+        }
+        const int *idx = sh.row_idx[vals][j & 1];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int r = r0 + i * RSTEP, x = idx[r];
+          cp_async16(at(i, r), base + (uint64_t)(uint32_t)max(x, 0) * (CPR * 16) + pc * 16, x >= 0);
+        }
+      };
       int st = 0, wrap = 1;  // ring stage of chunk j, parity of its release
       auto advance = [&]() {
         if (++st == nst) st = 0, wrap ^= 1;
       };
       if (!FP8) {
-        int tok = listed(0), marked = 0;
-        auto mark = [&](int upto) {  // chunks whose rows have landed
-          for (; marked < upto; ++marked) mbar_arrive(&full[marked % nst]);
-        };
-        for (; j < n; ++j) {
+        int tok = listed(0);
+        for (int j = 0; j < n; ++j) {
           const int row = row_of(j, tok);
           tok = listed(j + 1);
-          if (j >= nst && !mbar_test(&empty[st], wrap)) {
-            // about to wait: hand over what is on its way first
-            cp_async_wait<0>();
-            mark(j);
-            if (!wait_bar(&empty[st], wrap, abort, c)) break;
-          }
+          if (j >= nst && !wait_bar(&empty[st], wrap, abort, c)) break;
           if (!place(j, row)) break;
           const uint32_t dst = smem_addr(ring + st * TILE);
-          const int *idx = sh.row_idx[vals][j & 1];
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int r = r0 + i * RSTEP, x = idx[r];
-            cp_async16(dst + tile_at(r, pc, BLK), base + (uint64_t)(uint32_t)max(x, 0) * (CPR * 16) + pc * 16, x >= 0);
-          }
-          cp_async_commit();
-          if (j >= 1) {
-            cp_async_wait<1>();
-            mark(j);
-          }
+          copy(j, [&](int, int r) { return dst + tile_at(r, pc, BLK); });
+          cp_async_arrive(&full[st]);
+          if (notes) mbar_arrive(&full[st]);
           advance();
         }
-        cp_async_wait<0>();
-        if (j == n) mark(n);
+        asm volatile("cp.async.wait_all;" ::: "memory");  // no copy in flight past here
       } else {
-        uint4 raw[PER];
-        float sck = 0.f, scv = 0.f;
-        auto load = [&](int jj, int row) -> bool {  // chunk jj's pieces and this thread's scales
-          if (!place(jj, row)) return false;
-          const int *idx = sh.row_idx[vals][jj & 1];
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int x = idx[r0 + i * RSTEP];
-            raw[i] = x >= 0 ? __ldg(reinterpret_cast<const uint4 *>(base + (uint64_t)(uint32_t)x * (CPR * 16) + pc * 16))
-                            : make_uint4(0u, 0u, 0u, 0u);
+        // codes: NR tiles on their way, each thread its own pieces
+        constexpr int NR = F::NR;
+        uint8_t *raw = raw_s + (vals ? NR * F::RAW : 0);
+        int tok = listed(0);
+        auto bring = [&](int j) -> bool {
+          const int row = row_of(j, tok);
+          tok = listed(j + 1);
+          if (j < n) {
+            if (!place(j, row)) return false;
+            const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW) + pt * 16;
+            copy(j, [&](int i, int) { return dst + i * 2048; });
           }
-          if (vals) {
-            sck = row >= 0 ? c.k_scale[srow + row] : 0.f;
-            scv = row >= 0 ? c.v_scale[srow + row] : 0.f;
-          }
+          cp_async_commit();
           return true;
         };
-        int tok = listed(0);
-        bool ok = n > 0 && load(0, row_of(0, tok));
-        tok = listed(1);
-        for (; j < n && ok; ++j) {
-          if (j >= nst && !wait_bar(&empty[st], wrap, abort, c)) break;
+        bool ok = true;
+        for (int j = 0; j < NR - 1 && ok; ++j) ok = bring(j);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!(ok = bring(j + NR - 1))) break;
+          cp_async_wait<NR - 1>();
+          if (j >= nst && !(ok = wait_bar(&empty[st], wrap, abort, c))) break;
+          const uint8_t *from = raw + (j % NR) * F::RAW + pt * 16;
           uint8_t *dst = ring + st * TILE;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 2048);
             const int r = r0 + i * RSTEP;
             uint32_t w[8];
-            widen(raw[i].x, w[0], w[1]), widen(raw[i].y, w[2], w[3]);
-            widen(raw[i].z, w[4], w[5]), widen(raw[i].w, w[6], w[7]);
+            widen(v.x, w[0], w[1]), widen(v.y, w[2], w[3]), widen(v.z, w[4], w[5]), widen(v.w, w[6], w[7]);
             *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc, BLK)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc + 1, BLK)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
-          if (vals) sh.ks[j & (SLOTS - 1)][pt] = sck, sh.vs[j & (SLOTS - 1)][pt] = scv;
           umma::fence_proxy_async();
           mbar_arrive(&full[st]);
           advance();
-          if (j + 1 < n) {
-            const int row = row_of(j + 1, tok);
-            tok = listed(j + 2);
-            ok = load(j + 1, row);
-          }
         }
+        cp_async_wait<0>();
       }
     } else if (warp == MMA_WARP) {
       // ---- MMA issuer ----
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           const uint32_t va = smem_addr(v_s + st * TILE);
 #pragma unroll
           for (int kk = 0; kk < TOK / 16; ++kk)
-            mma_ts(tmem + T_O, tmem + T_P + b * 64 + kk * 8, desc_mn(va + kk * 2048, BLK), IDO);
+            mma_ts(tmem + T_O, tmem + T_P + b * (TOK / 2) + kk * 8, desc_mn(va + kk * 2048, BLK), IDO);
           umma::commit(&sh.vempty[st]);
           umma::commit(&sh.pvdone[b]);
         };
@@ -396,9 +420,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           const uint32_t ka = smem_addr(k_s + st * TILE);
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t at = (kk >> 2) * BLK + (kk & 3) * 32;
-            umma::mma<false>(tmem + T_S + b * 128, umma::smem_desc_sw128(qa + at), umma::smem_desc_sw128(ka + at), IDS,
-                             kk ? 1u : 0u);
+            const uint32_t at = (kk & 3) * 32;
+            umma::mma<false>(tmem + T_S + b * TOK, umma::smem_desc_sw128(qa + (kk >> 2) * F::QBLK + at),
+                             umma::smem_desc_sw128(ka + (kk >> 2) * BLK + at), IDS, kk ? 1u : 0u);
           }
           umma::commit(&sh.kempty[st]);
           umma::commit(&sh.sfull[b]);
@@ -439,10 +463,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         if (!ok) break;
         umma::fence_after();
         // ---- what this row sees ----
-        uint32_t see[4];
+        uint32_t see[W];
         bool masked = false;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < W; ++w) {
           uint32_t v = sh.have[slot][w];
           if (!LIST) {
             if (ck < c1) {
@@ -463,13 +487,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           masked |= v != 0xffffffffu;
         }
         masked = __any_sync(0xffffffffu, masked);
-        const uint32_t ts = tl + T_S + b * 128, tp = tl + T_P + b * 64;
-        const float *ks = sh.ks[slot], *vs = sh.vs[slot];
+        const uint32_t ts = tl + T_S + b * TOK, tp = tl + T_P + b * (TOK / 2);
+        const float *ks = scales.k[FP8 ? slot : 0], *vs = scales.v[FP8 ? slot : 0];
 
         auto weigh = [&](auto mk, float &sum) -> float {
           float top = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < W; ++w) {
             uint32_t v[32];
             umma::ld32(ts + w * 32, v);
             umma::ld_wait();
@@ -507,11 +531,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         if (__any_sync(0xffffffffu, top > LAZY)) {
           float mx = NEG_INF, my = NEG_INF;
 #pragma unroll 1
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < W; ++w) {
             uint32_t v[32];
             umma::ld32(ts + w * 32, v);
             umma::ld_wait();
-            const uint32_t sw = w == 0 ? see[0] : w == 1 ? see[1] : w == 2 ? see[2] : see[3];
+            const uint32_t sw = w == 0 ? see[0] : see[1];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float x = (sw >> i) & 1u ? __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] * row_mul : row_mul) : NEG_INF;
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             if (!(ok = meet())) break;
             if (tid == 0) sh.n_bad = 0;
             if (!(ok = meet())) break;
-            for (int p = 0; p < DH / 8; ++p) {
+            for (int p = 0; p < (tid < TOK ? DH / 8 : 0); ++p) {
               uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(tid, p, BLK));
               const uint4 q = *reinterpret_cast<const uint4 *>(e);
               const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -592,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             left = sh.n_bad;
             for (int i = 0; i < min(left, BAD); ++i) {
               const int2 at = sh.bad_at[i];
-              const uint32_t sw = at.x < 32 ? see[0] : at.x < 64 ? see[1] : at.x < 96 ? see[2] : see[3];
+              const uint32_t sw = at.x < 32 ? see[0] : see[1];
               const uint32_t ov = ld1(tl + T_O + at.y);
               const bool mine = (sw >> (at.x & 31)) & 1u;
               st1(tl + T_O + at.y, mine ? __float_as_uint(__uint_as_float(ov) + sh.bad_val[i]) : ov);
@@ -642,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
     t = find_tile<256>(a, per, tile_i);
     if (t.n == 0) break;
     if (tid == 0) {
-      for (int i = 0; i < 6; ++i) {
+      for (int i = 0; i < MAX_STAGES; ++i) {
         mbar_inval(&sh.kfull[i]), mbar_inval(&sh.vfull[i]), mbar_inval(&sh.kempty[i]), mbar_inval(&sh.vempty[i]);
       }
       for (int i = 0; i < 2; ++i) {
