@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
   const int row_tile = blockIdx.x % row_tiles, g0 = row_tile * R;
   int tile_i = blockIdx.x / row_tiles;
   const int tile_step = gridDim.x / row_tiles;
-  Tile t = {tile_i, 1};
+  Tile t = {tile_i, 1, 0};
   if (!LIST) t = find_tile<F::THREADS>(a, per, tile_i);
 
   for (; t.n > 0;) {
@@ -654,9 +654,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       }
       cluster_sync();  // no CTA overwrites or leaves what another still reads
     }
-    if (LIST) break;
-    __syncthreads();
     tile_i += tile_step;
+    if (LIST || tile_i >= t.total) break;
+    __syncthreads();
     t = find_tile<F::THREADS>(a, per, tile_i);
   }
 }
@@ -693,7 +693,8 @@ struct Plan {
 // Rows of a tile: as many n-tiles as one query's G heads (and, without lists,
 // its sequence's neighbours) fill, 32 rows at the most.  Lengths are on the
 // device: whole prefixes count as full caches, and the batch's queries as
-// spread evenly over the sequences.
+// spread evenly over the sequences (a CTA goes on to the tiles beyond the
+// grid where they are not).
 Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   Plan p;
   const int G = H / c.H_kv;
@@ -704,9 +705,9 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   if (p.umma) {
     p.nr = 0, p.row_tiles = 1, p.cluster = false;
     p.per = list ? 1 : 128 / G;
-    p.tiles = list ? n_q : std::min(n_q, cdiv(n_q, p.per) + seqs);
+    p.tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
     const int chunks = cdiv(list ? k : c.L_cap, 64) + cdiv(n_draft, 64);
-    const int64_t units = (int64_t)(list ? n_q : seqs * cdiv(per_seq, p.per)) * c.H_kv;
+    const int64_t units = (int64_t)p.tiles * c.H_kv;
     // shares: the fewest chunk times over the waves of one CTA per SM, with
     // about 12 chunks' time for a CTA's beginning and end
     const int sms = device_sms();
@@ -722,11 +723,10 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   const int R = 8 * p.nr;
   p.per = list ? 1 : std::max(1, R / G);
   p.row_tiles = p.per > 1 ? 1 : cdiv(G, R);
-  p.tiles = list ? n_q : std::min(n_q, cdiv(n_q, p.per) + seqs);
-  const int tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
+  p.tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
   const int ch = chunk_tokens(c.fp8, p.nr), chunks = cdiv(list ? k : c.L_cap, ch) + cdiv(n_draft, ch);
   const int ctas = ctas_per_sm(c.fp8, c.d, p.nr);
-  const int64_t units = (int64_t)tiles * p.row_tiles * c.H_kv;
+  const int64_t units = (int64_t)p.tiles * p.row_tiles * c.H_kv;
   // shares: fill the SMs once, two chunks per warp at the least.  A cluster of
   // up to 8 joins them without a second launch; more shares pay off only
   // where each of 8 would still run through 32 chunks per warp or more.

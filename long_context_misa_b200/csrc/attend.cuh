@@ -60,9 +60,10 @@ __device__ __forceinline__ int attend_prefix(const KvView &c, const AttendView &
   return p + 1;
 }
 
-// Queries [q0, q0 + n) of one sequence that a tile holds.
+// Queries [q0, q0 + n) of one sequence that a tile holds, and the batch's
+// number of tiles.
 struct Tile {
-  int q0, n;
+  int q0, n, total;
 };
 
 // Tile number `want` of the batch without lists: runs of neighbouring queries
@@ -76,7 +77,8 @@ __device__ Tile find_tile(const AttendView &a, int per, int want) {
   __shared__ int part[NWARP + 1];
   __shared__ Tile found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found = {0, 0};
+  if (tid == 0) found = {0, 0, 0};
+  int tiles = 0;
   for (int base = 0; base < a.n_q; base += SPAN) {
     const int m = min(SPAN, a.n_q - base);
     __syncthreads();
@@ -127,18 +129,18 @@ __device__ Tile find_tile(const AttendView &a, int per, int want) {
 #pragma unroll
     for (int e = 0; e < PER_T; ++e) {
       if (!is[e]) continue;
-      if (first++ == want) {
+      if (tiles + first++ == want) {
         const int i = tid * PER_T + e;
         int n = 1;
         while (n < per && i + n < m && seq_s[i + n] == seq_s[i]) ++n;
-        found = {base + i, n};
+        found = {base + i, n, 0};
       }
     }
-    if (want < total) break;
-    want -= total;
+    tiles += total;
   }
   __syncthreads();
-  const Tile t = found;
+  Tile t = found;
+  t.total = tiles;
   __syncthreads();
   return t;
 }
@@ -205,7 +207,7 @@ __device__ __forceinline__ float4 ld_cluster(const void *p, uint32_t rank) {
 
 // attend_umma.cu: the same attention for tiles of many rows (more than 32 heads
 // of a query, or of neighbouring queries of one sequence) on tcgen05 tensor
-// cores.  per: queries per tile; tiles: upper bound of the tiles.
+// cores.  per: queries per tile; tiles: CTAs in x (each goes on by that many).
 cudaError_t launch_attend_umma(const KvView &c, const AttendView &a, const Split &sp, int per, int tiles,
                                cudaStream_t s);
 

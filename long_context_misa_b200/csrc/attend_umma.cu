@@ -5,20 +5,22 @@
 //
 // A CTA holds up to 128 rows (lanes of tensor memory) of one key/value head
 // and a share of the tokens, in chunks of 64:
-//   8 producer warps   gather a chunk's keys (4 warps) and values (4) into
+//   4 producer warps   gather a chunk's keys (2 warps) and values (2) into
 //                      rings of 128-byte-swizzled tiles: cp.async for bf16
 //                      rows; e4m3 rows go through a ring of their own and are
 //                      widened to f16 by the threads that brought them
-//   1 MMA thread       S_j = Q K_j^T and O += P_j V_j (V as the MN-major
-//                      operand, P from tensor memory), S_(j+1) before P_j V_j
-//   4 softmax warps    one row per thread: S from tensor memory, weights back
-//                      into it, the running sum; O is touched only when a
-//                      weight passes 256 times its reference
-// Tensor memory: O [0, 128), two S of 64 columns, two P of 32.  A tile of 64
-// tokens (32 KB bf16) costs 512 cycles of MMA at M = 128 and about 550 of
-// softmax issue beside them, against 1425 cycles of its share of HBM.  Tiles
-// of 64 tokens keep less of the rings waiting than tiles of 128 (measured:
-// see TOK).
+//   1 MMA thread       S_j = Q K_j^T, two chunks ahead of O += P_j V_j (V as
+//                      the MN-major operand, P from tensor memory)
+//   2 x 4 softmax warps, one row per thread: the even and the odd chunks, each
+//                      with its own O and running maximum, so that neither
+//                      waits for the other; they join at the end.  Weights go
+//                      back into the columns of S; O is touched only when a
+//                      weight passes 256 times its reference.
+// Tensor memory: two O of 128 columns, four S (then P) of 64.
+// A chunk (32 KB of bf16 rows) is 512 cycles of MMA at M = 128 and 1425 of the
+// SM's share of HBM; a softmax warp needs about 1500 cycles for it (mostly
+// latencies), which one set of warps could not hide (measured: 24 queries x 4
+// heads over 32K bf16 tokens of 4 sequences: 163 us with one set).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -30,10 +32,11 @@ namespace {
 constexpr int M = 128, TOK = 64;  // rows and tokens of a tile
 constexpr int W = TOK / 32;        // mask words of a tile
 constexpr int WARPS = 13, THREADS = WARPS * 32;
-constexpr int PROD0 = 4, MMA_WARP = 12;  // warps 4..7 keys, 8..11 values
+constexpr int PROD0 = 8, MMA_WARP = 12;  // warps 0..7 softmax, 8 and 9 keys, 10 and 11 values
+constexpr int GROUP = 64;                // threads of a producer group
 constexpr int SLOTS = 32;                // masks and scales in flight (more than the rings can be ahead)
-constexpr int T_O = 0, T_S = 128, T_P = 256, T_COLS = 512;
-constexpr int BAD = 256;  // non-finite values handled per round
+constexpr int T_O = 0, T_S = 256, T_COLS = 512;  // O of set g at 128 g, S of chunk j at 256 + 64 (j & 3)
+constexpr int BAD = 128;  // non-finite values handled per round
 
 template <int DH_, bool FP8_>
 struct UCfg {
@@ -43,28 +46,30 @@ struct UCfg {
   static constexpr int BLK = TOK * 128;      // its blocks of 64 elements
   static constexpr int QBLK = M * 128, QTILE = M * DH * 2;
   static constexpr int CPR = DH * (FP8 ? 1 : 2) / 16;  // 16-byte pieces of a row as stored
-  static constexpr int PER = TOK * CPR / 128;          // of them per producer thread and tile
+  static constexpr int PER = TOK * CPR / GROUP;        // of them per producer thread and tile
   static constexpr int RAW = FP8 ? TOK * DH : 0;       // a tile of codes
   // ring stages: operand tiles of keys and values, tiles of codes of either
-  static constexpr int NK = FP8 ? 2 : DH > 64 ? 4 : 8, NV = FP8 ? 3 : DH > 64 ? 6 : 10, NR = FP8 ? (DH > 64 ? 5 : 8) : 0;
+  static constexpr int NK = FP8 ? 3 : DH > 64 ? 4 : 8, NV = FP8 ? 3 : DH > 64 ? 6 : 10, NR = FP8 ? (DH > 64 ? 4 : 8) : 0;
   static constexpr int SMEM = QTILE + (NK + NV) * TILE + 2 * NR * RAW + 1024;
-  static_assert(NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
+  static_assert((NK + NV) * TILE >= M * (DH * 4 + 16), "the odd set's result takes the rings' place");
+  static_assert(GROUP == TOK && NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
 };
 constexpr int MAX_STAGES = 10;
 
 struct Shared {
   uint64_t kfull[MAX_STAGES], kempty[MAX_STAGES], vfull[MAX_STAGES], vempty[MAX_STAGES];
-  uint64_t sfull[2], sfree[2], pfull[2], pvdone[2], done;
-  uint64_t placed[2], scan;  // meetings of a producer group, of the softmax warps
+  uint64_t sfull[4], pfull[4], pvdone[2], done;
+  uint64_t placed[2], scan[2], joined;  // meetings of a producer group, a softmax set, both sets
   uint32_t tmem_base;
   int abort;
   int row_idx[2][2][TOK];   // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
   uint32_t have[SLOTS][W];  // which tokens of a chunk are there
   int len[M], query[M];
+  float mul[M];  // scale log2(e), over the row's power of two (e4m3 caches)
   int seq, max_len, min_len;
-  int n_bad;
-  int2 bad_at[BAD];  // (token, element)
-  float bad_val[BAD];
+  int n_bad[2];
+  int2 bad_at[2][BAD];  // (token, element)
+  float bad_val[2][BAD];
 };
 
 template <bool FP8>
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
   volatile int *abort = &sh.abort;
 
   int tile_i = blockIdx.x;
-  Tile t = {tile_i, 1};
+  Tile t = {tile_i, 1, 0};
   if (!LIST) t = find_tile<256>(a, per, tile_i);
   if (t.n == 0) return;  // the whole CTA, before anything is allocated
 
@@ -169,15 +174,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       for (int i = 0; i < MAX_STAGES; ++i) {
         // every producer thread of the group (bf16: as its copies land, and
         // the lanes that noted the masks)
-        mbar_init(&sh.kfull[i], 128), mbar_init(&sh.vfull[i], FP8 ? 128 : 128 + W);
-        mbar_init(&sh.kempty[i], 1), mbar_init(&sh.vempty[i], 1);    // the MMAs' commit
+        mbar_init(&sh.kfull[i], GROUP), mbar_init(&sh.vfull[i], FP8 ? GROUP : GROUP + W);
+        mbar_init(&sh.kempty[i], 1), mbar_init(&sh.vempty[i], 1);  // the MMAs' commit
       }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sh.sfull[i], 1), mbar_init(&sh.pvdone[i], 1);
-        mbar_init(&sh.sfree[i], 128), mbar_init(&sh.pfull[i], 128);  // every softmax thread
-      }
-      mbar_init(&sh.done, 1);
-      mbar_init(&sh.placed[0], 128), mbar_init(&sh.placed[1], 128), mbar_init(&sh.scan, 128);
+      for (int i = 0; i < 4; ++i) mbar_init(&sh.sfull[i], 1), mbar_init(&sh.pfull[i], 128);  // a softmax set
+      for (int i = 0; i < 2; ++i)
+        mbar_init(&sh.pvdone[i], 1), mbar_init(&sh.placed[i], GROUP), mbar_init(&sh.scan[i], 128);
+      mbar_init(&sh.done, 1), mbar_init(&sh.joined, 256);
       fence_mbar_init();
       sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff;
     }
@@ -196,42 +199,35 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       sh.query[tid] = tid < n_rows ? row_query(tid) : -1;
     }
     // ---- Q: 16-bit rows, K-major with 128-byte swizzle; e4m3 caches: f16
-    // after a power of two per row ----
-    float row_mul = a.scale * LOG2E;
-    if (tid < M) {
-      const bool live = tid < n_rows;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          a.q + ((int64_t)row_query(live ? tid : 0) * a.H + row_head(live ? tid : 0)) * DH);
-      float sc = 1.f;
-      if (FP8 && live) {
+    // after a power of two per row.  DH / 8 lanes hold a row ----
+    constexpr int QL = DH / 8;
+    for (int e = tid; e < (M * QL + THREADS - 1) / THREADS * THREADS; e += THREADS) {
+      const int r = min(e / QL, M - 1), p = e % QL;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (e < M * QL && r < n_rows)
+        v = reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH)[p];
+      if (FP8) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float m = 0.f;
-        for (int p = 0; p < DH / 8; ++p) {
-          const uint4 v = src[p];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        auto take = [&](float x) { m = (x > m || x != x) ? x : m; };  // a NaN stays
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = bf16x2_to_float2(w[i]);
-            const float x = fabsf(f.x), y = fabsf(f.y);
-            m = (x > m || x != x) ? x : m;  // a NaN stays
-            m = (y > m || y != y) ? y : m;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(w[i]);
+          take(fabsf(f.x));
+          take(fabsf(f.y));
         }
-        sc = row_scale(m);
-        row_mul = a.scale * LOG2E / sc;
-      }
-      for (int p = 0; p < DH / 8; ++p) {
-        uint4 v = live ? src[p] : make_uint4(0u, 0u, 0u, 0u);
-        if (FP8) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = bf16x2_to_float2(w[i]);
-            w[i] = f16x2(f.x * sc, f.y * sc);
-          }
-          v = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int o = 1; o < QL; o <<= 1) take(__shfl_xor_sync(0xffffffffu, m, o));
+        const float sc = row_scale(m);
+        if (p == 0 && e < M * QL) sh.mul[r] = a.scale * LOG2E / sc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(w[i]);
+          w[i] = f16x2(f.x * sc, f.y * sc);
         }
-        *reinterpret_cast<uint4 *>(q_s + tile_at(tid, p, F::QBLK)) = v;
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if (e < M * QL) *reinterpret_cast<uint4 *>(q_s + tile_at(r, p, F::QBLK)) = v;
     }
     umma::fence_proxy_async();
     umma::fence_before();
@@ -249,15 +245,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
 
     if (warp >= PROD0 && warp < MMA_WARP) {
       // ---- producers ----
-      const bool vals = warp >= PROD0 + 4;
-      const int pt = (tid - PROD0 * 32) & 127, lt = pt & (TOK - 1);  // (threads beyond TOK repeat the first ones' tokens)
+      const bool vals = warp >= PROD0 + 2;
+      const int pt = (tid - PROD0 * 32) & (GROUP - 1);
       uint64_t *full = vals ? sh.vfull : sh.kfull, *empty = vals ? sh.vempty : sh.kempty;
       const uint8_t *base = (vals ? c.v : c.k) + (int64_t)max(seq, 0) * c.L_cap * c.H_kv * (CPR * 16);
       const int64_t srow = (int64_t)max(seq, 0) * c.L_cap * c.H_kv;
       uint8_t *ring = vals ? v_s : k_s;
       const int nst = vals ? NV : NK;
-      auto listed = [&](int j) -> int {  // token lt of chunk j as listed
-        const int i = (cb + j) * TOK + lt;
+      auto listed = [&](int j) -> int {  // token pt of chunk j as listed
+        const int i = (cb + j) * TOK + pt;
         if (!LIST) return i;
         return j < n && i < a.k ? __ldg(a.topk + (int64_t)t.q0 * a.k + i) : -1;
       };
@@ -266,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         if (cb + j < c1) {
           if (tok < 0 || tok >= max_len) return -1;
         } else {
-          const int d = (cb + j - c1) * TOK + lt;
+          const int d = (cb + j - c1) * TOK + pt;
           if (d >= n_draft) return -1;
           if (LIST && !((a.draft_mask[(int64_t)t.q0 * words + (d >> 5)] >> (d & 31)) & 1u)) return -1;
           const int64_t p = (int64_t)draft0 + d;
@@ -281,11 +277,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       // rows of chunk j into row_idx[..][j & 1]; the values' group also notes
       // which are there and (e4m3) brings the scales, for the softmax warps,
       // who wait for the values' tile
-      const bool notes = vals && pt < TOK && lane == 0;
+      const bool notes = vals && lane == 0;
       int meetings = 0;
       auto bring_scale = [&](int j, int row) {
-        float(*to)[TOK] = pt < TOK ? scales.k : scales.v;
-        cp_async4(smem_addr(&to[j & (SLOTS - 1)][lt]), (pt < TOK ? c.k_scale : c.v_scale) + srow + max(row, 0), row >= 0);
+        cp_async4(smem_addr(&scales.k[j & (SLOTS - 1)][pt]), c.k_scale + srow + max(row, 0), row >= 0);
+        cp_async4(smem_addr(&scales.v[j & (SLOTS - 1)][pt]), c.v_scale + srow + max(row, 0), row >= 0);
       };
       auto place = [&](int j, int row) -> bool {
         if (!LIST && cb + j < c1) {
@@ -294,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           if (FP8 && vals) bring_scale(j, row);
           return true;
         }
-        if (pt < TOK) sh.row_idx[vals][j & 1][pt] = row;
+        sh.row_idx[vals][j & 1][pt] = row;
         const uint32_t b = __ballot_sync(0xffffffffu, row >= 0);
         if (notes) sh.have[j & (SLOTS - 1)][pt >> 5] = b;
         if (FP8 && vals) bring_scale(j, row);
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         return wait_bar(&sh.placed[vals], meetings++ & 1, abort, c);
       };
       const int pc = pt % CPR, r0 = pt / CPR;
-      constexpr int RSTEP = 128 / CPR;
+      constexpr int RSTEP = GROUP / CPR;
       // whether chunk j is a stretch of the prefix: its rows need no list, and
       // no meeting of the group to share one
       auto stretch = [&](int j) { return !LIST && cb + j < c1; };
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           if (j < n) {
             if (!place(j, row)) return false;
             const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW) + pt * 16;
-            copy(j, [&](int i, int) { return dst + i * 2048; });
+            copy(j, [&](int i, int) { return dst + i * (GROUP * 16); });
           }
           cp_async_commit();
           return true;
@@ -376,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           uint8_t *dst = ring + st * TILE;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 2048);
+            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * (GROUP * 16));
             const int r = r0 + i * RSTEP;
             uint32_t w[8];
             widen(v.x, w[0], w[1]), widen(v.y, w[2], w[3]), widen(v.z, w[4], w[5]), widen(v.w, w[6], w[7]);
@@ -398,106 +394,118 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
                                  ((uint32_t)(M >> 4) << 24);
         const uint32_t qa = smem_addr(q_s);
         bool ok = true;
-        auto pv = [&](int j) {
-          const int st = j % NV, b = j & 1;
-          ok = ok && wait_bar(&sh.vfull[st], (j / NV) & 1, abort, c) && wait_bar(&sh.pfull[b], (j >> 1) & 1, abort, c);
+        auto s_of = [&](int j) {
+          const int st = j % NK;
+          // the columns held P_(j-4)
+          if (j >= 4) ok = ok && wait_bar(&sh.pvdone[j & 1], ((j - 4) >> 1) & 1, abort, c);
+          ok = ok && wait_bar(&sh.kfull[st], (j / NK) & 1, abort, c);
           if (!ok) return;
-          umma::fence_proxy_async();
-          umma::fence_after();
-          const uint32_t va = smem_addr(v_s + st * TILE);
-#pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk)
-            mma_ts(tmem + T_O, tmem + T_P + b * (TOK / 2) + kk * 8, desc_mn(va + kk * 2048, BLK), IDO);
-          umma::commit(&sh.vempty[st]);
-          umma::commit(&sh.pvdone[b]);
-        };
-        for (int j = 0; j < n && ok; ++j) {
-          const int st = j % NK, b = j & 1;
-          ok = wait_bar(&sh.kfull[st], (j / NK) & 1, abort, c) && (j < 2 || wait_bar(&sh.sfree[b], ((j >> 1) & 1) ^ 1, abort, c));
-          if (!ok) break;
           umma::fence_proxy_async();
           umma::fence_after();
           const uint32_t ka = smem_addr(k_s + st * TILE);
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) {
             const uint32_t at = (kk & 3) * 32;
-            umma::mma<false>(tmem + T_S + b * TOK, umma::smem_desc_sw128(qa + (kk >> 2) * F::QBLK + at),
+            umma::mma<false>(tmem + T_S + (j & 3) * TOK, umma::smem_desc_sw128(qa + (kk >> 2) * F::QBLK + at),
                              umma::smem_desc_sw128(ka + (kk >> 2) * BLK + at), IDS, kk ? 1u : 0u);
           }
           umma::commit(&sh.kempty[st]);
-          umma::commit(&sh.sfull[b]);
-          if (j > 0) pv(j - 1);
+          umma::commit(&sh.sfull[j & 3]);
+        };
+        auto pv = [&](int j) {
+          const int st = j % NV;
+          ok = ok && wait_bar(&sh.vfull[st], (j / NV) & 1, abort, c) && wait_bar(&sh.pfull[j & 3], (j >> 2) & 1, abort, c);
+          if (!ok) return;
+          umma::fence_proxy_async();
+          umma::fence_after();
+          const uint32_t va = smem_addr(v_s + st * TILE);
+#pragma unroll
+          for (int kk = 0; kk < TOK / 16; ++kk)
+            mma_ts(tmem + T_O + (j & 1) * 128, tmem + T_S + (j & 3) * TOK + kk * 8, desc_mn(va + kk * 2048, BLK), IDO);
+          umma::commit(&sh.vempty[st]);
+          umma::commit(&sh.pvdone[j & 1]);
+        };
+        s_of(0);
+        if (n > 1) s_of(1);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 2 < n) s_of(j + 2);
+          pv(j);
         }
-        if (ok) pv(n - 1);
         // nothing in flight past here (bounded)
         umma::commit(&sh.done);
         mbar_wait(&sh.done, 0);
       }
     } else {
-      // ---- softmax: row tid ----
-      const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-      const int my_len = sh.len[tid], my_query = sh.query[tid];
+      // ---- softmax: row tid % 128, chunks g, g + 2, ... ----
+      const int g = warp >> 2, r = tid & 127;
+      const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = tl + T_O + g * 128;
+      const int my_len = sh.len[r], my_query = sh.query[r];
+      const float row_mul = FP8 ? sh.mul[r] : a.scale * LOG2E;
       float m_ref = NEG_INF, y_ref = NEG_INF, fac = 1.f, l_sum = 0.f;
       bool ok = true;
       int scans = 0;
       // bounded waits of a whole warp (its tensor-memory accesses need all lanes)
       auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, c)) != 0; };
-      auto meet = [&]() {  // the 128 softmax threads
-        mbar_arrive(&sh.scan);
-        return wait(&sh.scan, scans++ & 1);
+      auto meet = [&]() {  // the 128 threads of the set
+        mbar_arrive(&sh.scan[g]);
+        return wait(&sh.scan[g], scans++ & 1);
       };
       {
         const uint32_t zero[16] = {};
 #pragma unroll
-        for (int i = 0; i < DH; i += 16) st16(tl + T_O + i, zero);
+        for (int i = 0; i < DH; i += 16) st16(to + i, zero);
         st_wait();
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int b = j & 1, slot = j & (SLOTS - 1), ck = cb + j;
-        ok = wait(&sh.sfull[b], (j >> 1) & 1);
-        // P_(j-2) has been used
-        if (ok && j >= 2) ok = wait(&sh.pvdone[b], ((j >> 1) & 1) ^ 1);
-        // the chunk's masks and scales come with its values (whose stage is
-        // not filled again before this chunk is done)
-        if (ok) ok = wait(&sh.vfull[j % NV], (j / NV) & 1);
+      for (int j = g; j < n && ok; j += 2) {
+        const int slot = j & (SLOTS - 1), ck = cb + j;
+        ok = wait(&sh.sfull[j & 3], (j >> 2) & 1);
+        // the masks and scales come with the chunk's values (whose stage is
+        // not filled again before this chunk is done); a stretch of the prefix
+        // needs no mask from there
+        const bool stretch = !LIST && ck < c1;
+        if (ok && (FP8 || !stretch)) ok = wait(&sh.vfull[j % NV], (j / NV) & 1);
         if (!ok) break;
         umma::fence_after();
         // ---- what this row sees ----
         uint32_t see[W];
         bool masked = false;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          uint32_t v = sh.have[slot][w];
-          if (!LIST) {
-            if (ck < c1) {
-              const int nn = my_len - ck * TOK - w * 32;
-              v &= nn >= 32 ? 0xffffffffu : nn > 0 ? (1u << nn) - 1u : 0u;
-            } else if (my_len < 0) {
-              v = 0u;
-            } else {
-              const int d0 = (ck - c1) * TOK + w * 32;
-              uint32_t m = d0 < n_draft ? a.draft_mask[(int64_t)my_query * words + (d0 >> 5)] : 0u;
-              if (n_draft - d0 < 32) m &= n_draft > d0 ? (1u << (n_draft - d0)) - 1u : 0u;
-              if (m & ~v) flag(c, MISA_DEV_BAD_POSITION);
-              v &= m;
-            }
-          }
-          if (tid >= n_rows) v = sh.have[slot][w];  // nobody reads these rows
-          see[w] = v;
-          masked |= v != 0xffffffffu;
-        }
-        masked = __any_sync(0xffffffffu, masked);
-        const uint32_t ts = tl + T_S + b * TOK, tp = tl + T_P + b * (TOK / 2);
-        const float *ks = scales.k[FP8 ? slot : 0], *vs = scales.v[FP8 ? slot : 0];
-
-        auto weigh = [&](auto mk, float &sum) -> float {
-          float top = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
+        if (stretch) {
+          const int left = (r < n_rows ? my_len : max_len) - ck * TOK;
+          see[0] = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+          see[1] = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1u : 0u;
+          masked = left < TOK;
+        } else {
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            uint32_t v[32];
-            umma::ld32(ts + w * 32, v);
-            umma::ld_wait();
-            uint32_t pk[16];
+            uint32_t v = sh.have[slot][w];
+            if (!LIST && r < n_rows) {  // (nobody reads the other rows)
+              if (my_len < 0) {
+                v = 0u;
+              } else {
+                const int d0 = (ck - c1) * TOK + w * 32;
+                uint32_t m = d0 < n_draft ? a.draft_mask[(int64_t)my_query * words + (d0 >> 5)] : 0u;
+                if (n_draft - d0 < 32) m &= n_draft > d0 ? (1u << (n_draft - d0)) - 1u : 0u;
+                if (m & ~v) flag(c, MISA_DEV_BAD_POSITION);
+                v &= m;
+              }
+            }
+            see[w] = v;
+            masked |= v != 0xffffffffu;
+          }
+        }
+        masked = __any_sync(0xffffffffu, masked);
+        const uint32_t ts = tl + T_S + (j & 3) * TOK;
+        const float *ks = scales.k[FP8 ? slot : 0], *vs = scales.v[FP8 ? slot : 0];
+
+        uint32_t pk[TOK / 2];  // P as it goes back to tensor memory
+        auto weigh = [&](auto mk, float &sum) -> float {
+          float top = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t v[W][32];
+#pragma unroll
+          for (int w = 0; w < W; ++w) umma::ld32(ts + w * 32, v[w]);
+          umma::ld_wait();
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               float k4[4] = {1.f, 1.f, 1.f, 1.f}, v4[4] = {1.f, 1.f, 1.f, 1.f}, wt[4];
@@ -509,25 +517,25 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               }
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                float x = fmaf(__uint_as_float(v[i + u]), FP8 ? k4[u] * row_mul : row_mul, -m_ref);
+                float x = fmaf(__uint_as_float(v[w][i + u]), FP8 ? k4[u] * row_mul : row_mul, -m_ref);
                 const bool seen = !mk.value || ((see[w] >> (i + u)) & 1u);
                 if (mk.value && !seen) x = NEG_INF;
                 const float p = ex2(x);
                 s4[u] += p;
                 wt[u] = p;
                 if (FP8) wt[u] = seen ? p * (v4[u] * fac) : 0.f;
-                top = fmaxf(top, fmaxf(p, wt[u]));
+                top = FP8 ? fmaxf(top, fmaxf(p, wt[u])) : fmaxf(top, p);
               }
 #pragma unroll
-              for (int u = 0; u < 4; u += 2) pk[(i + u) / 2] = FP8 ? f16x2(wt[u], wt[u + 1]) : bf16x2(wt[u], wt[u + 1]);
+              for (int u = 0; u < 4; u += 2)
+                pk[(w * 32 + i + u) / 2] = FP8 ? f16x2(wt[u], wt[u + 1]) : bf16x2(wt[u], wt[u + 1]);
             }
-            st16(tp + w * 16, pk);
           }
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
           return top;
         };
         float sum = 0.f, top = LAZY + 1.f;
-        if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
+        if (j > g) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
         if (__any_sync(0xffffffffu, top > LAZY)) {
           float mx = NEG_INF, my = NEG_INF;
 #pragma unroll 1
@@ -550,15 +558,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           const float m_new = fmaxf(m_ref, mx), y_new = fmaxf(y_ref, my);
           l_sum *= m_new == NEG_INF ? 1.f : ex2(m_ref - m_new);
           const float al = y_new == NEG_INF ? 1.f : ex2(y_ref - y_new);
-          if (j > 0) {
-            // O may change once P_(j-1) V_(j-1) is in it
-            ok = wait(&sh.pvdone[b ^ 1], ((j - 1) >> 1) & 1);
+          if (j > g) {
+            // O may change once P_(j-2) V_(j-2) is in it
+            ok = wait(&sh.pvdone[g], ((j - 2) >> 1) & 1);
             if (!ok) break;
             umma::fence_after();
 #pragma unroll 1
             for (int i = 0; i < DH; i += 32) {
               uint32_t v[32];
-              umma::ld32(tl + T_O + i, v);
+              umma::ld32(to + i, v);
               umma::ld_wait();
               uint32_t x[16], y[16];
 #pragma unroll
@@ -566,35 +574,37 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
                 x[u] = __float_as_uint(__uint_as_float(v[u]) * al);
                 y[u] = __float_as_uint(__uint_as_float(v[16 + u]) * al);
               }
-              st16(tl + T_O + i, x);
-              st16(tl + T_O + i + 16, y);
+              st16(to + i, x);
+              st16(to + i + 16, y);
             }
             st_wait();
           }
-          m_ref = m_new, y_ref = y_new;
+          y_ref = y_new;
           fac = m_new == NEG_INF || !FP8 ? 1.f : ex2(m_new - y_new);
           // a row that still sees nothing: its masked logits must not meet -inf
-          const float keep = m_ref;
-          if (m_ref == NEG_INF) m_ref = 0.f;
+          m_ref = m_new == NEG_INF ? 0.f : m_new;
           masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
-          m_ref = keep;
+          m_ref = m_new;
         }
         l_sum += sum;
+#pragma unroll
+        for (int i = 0; i < TOK / 2; i += 16) st16(ts + i, reinterpret_cast<const uint32_t(&)[16]>(pk[i]));
         // ---- values that some rows must not see: NaN and infinities there
         // would reach them as 0 * NaN.  They are taken out of the tile and
         // added to O in the rows that see them (a weight is positive) ----
         if (!LIST && (ck >= c1 || (ck + 1) * TOK > min_len)) {
-          if (j > 0) ok = wait(&sh.pvdone[b ^ 1], ((j - 1) >> 1) & 1);
+          ok = wait(&sh.vfull[j % NV], (j / NV) & 1);
+          if (ok && j > g) ok = wait(&sh.pvdone[g], ((j - 2) >> 1) & 1);
           umma::fence_after();
           uint8_t *vt = v_s + (j % NV) * TILE;
           constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u;
           int left = 0;
           while (ok) {
             if (!(ok = meet())) break;
-            if (tid == 0) sh.n_bad = 0;
+            if (r == 0) sh.n_bad[g] = 0;
             if (!(ok = meet())) break;
-            for (int p = 0; p < (tid < TOK ? DH / 8 : 0); ++p) {
-              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(tid, p, BLK));
+            for (int p = 0; p < (r < TOK ? DH / 8 : 0); ++p) {
+              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(r, p, BLK));
               const uint4 q = *reinterpret_cast<const uint4 *>(e);
               const uint32_t w[4] = {q.x, q.y, q.z, q.w};
               bool any = false;
@@ -604,22 +614,23 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               for (int i = 0; i < 8; ++i) {
                 const uint32_t bits = e[i];
                 if ((bits & EXP) != EXP) continue;
-                const int at = atomicAdd(&sh.n_bad, 1);
+                const int at = atomicAdd(&sh.n_bad[g], 1);
                 if (at >= BAD) continue;  // the next round's
-                sh.bad_at[at] = make_int2(tid, p * 8 + i);
+                sh.bad_at[g][at] = make_int2(r, p * 8 + i);
                 const uint32_t mant = bits & (FP8 ? 0x3ffu : 0x7fu);
-                sh.bad_val[at] = mant ? __int_as_float(0x7fffffff) : __int_as_float((bits & 0x8000u) ? 0xff800000u : 0x7f800000u);
+                sh.bad_val[g][at] =
+                    mant ? __int_as_float(0x7fffffff) : __int_as_float((bits & 0x8000u) ? 0xff800000u : 0x7f800000u);
                 e[i] = 0;
               }
             }
             if (!(ok = meet())) break;
-            left = sh.n_bad;
+            left = sh.n_bad[g];
             for (int i = 0; i < min(left, BAD); ++i) {
-              const int2 at = sh.bad_at[i];
+              const int2 at = sh.bad_at[g][i];
               const uint32_t sw = at.x < 32 ? see[0] : see[1];
-              const uint32_t ov = ld1(tl + T_O + at.y);
+              const uint32_t ov = ld1(to + at.y);
               const bool mine = (sw >> (at.x & 31)) & 1u;
-              st1(tl + T_O + at.y, mine ? __float_as_uint(__uint_as_float(ov) + sh.bad_val[i]) : ov);
+              st1(to + at.y, mine ? __float_as_uint(__uint_as_float(ov) + sh.bad_val[g][i]) : ov);
               st_wait();
             }
             if (left <= BAD) break;
@@ -629,50 +640,69 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         }
         st_wait();
         umma::fence_before();
-        mbar_arrive(&sh.sfree[b]);
-        mbar_arrive(&sh.pfull[b]);
+        mbar_arrive(&sh.pfull[j & 3]);
       }
+      // ---- the two sets' O meet where the rings were (every tile of them has
+      // been used once both sets' last products are done) ----
       if (ok && n > 0) ok = wait(&sh.pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1);
+      if (ok && n > 1) ok = wait(&sh.pvdone[n & 1], ((n - 2) >> 1) & 1);
       umma::fence_after();
-      // ---- this share of the rows ----
-      const bool live = ok && tid < n_rows;
-      const int64_t orow = live ? (int64_t)row_query(tid) * a.H + row_head(tid) : 0;
-      const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
+      float *other = reinterpret_cast<float *>(k_s);                 // [DH / 4][M] float4: thread by thread
+      float4 *other_ml = reinterpret_cast<float4 *>(k_s + M * DH * 4);  // [M]
+      const bool live = ok && r < n_rows;
+      if (g == 1 && ok) {
+        other_ml[r] = make_float4(m_ref, l_sum, y_ref, 0.f);
 #pragma unroll 1
-      for (int i = 0; i < DH; i += 32) {
-        uint32_t v[32];
-        umma::ld32(tl + T_O + i, v);
-        umma::ld_wait();
-        if (!live) continue;
+        for (int i = 0; i < DH; i += 32) {
+          uint32_t v[32];
+          umma::ld32(to + i, v);
+          umma::ld_wait();
 #pragma unroll
-        for (int u = 0; u < 32; u += 4) {
-          Part p;
-          p.M = m_ref, p.Y = y_ref, p.l = l_sum;
-          p.v = make_float4(__uint_as_float(v[u]), __uint_as_float(v[u + 1]), __uint_as_float(v[u + 2]), __uint_as_float(v[u + 3]));
-          if (Z == 1)
-            store_row(a, p, orow, DH, i + u);
-          else
-            *reinterpret_cast<float4 *>(split.o + prow * DH + i + u) = p.v;
+          for (int u = 0; u < 32; u += 4)
+            reinterpret_cast<uint4 *>(other)[((i + u) / 4) * M + r] = make_uint4(v[u], v[u + 1], v[u + 2], v[u + 3]);
         }
       }
-      if (live && Z > 1) split.ml[prow] = make_float4(m_ref, l_sum, y_ref, 0.f);
+      mbar_arrive(&sh.joined);
+      if (g == 0 && ok && (ok = wait(&sh.joined, 0))) {
+        const int64_t orow = live ? (int64_t)row_query(r) * a.H + row_head(r) : 0;
+        const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
+        const float4 mine = make_float4(m_ref, l_sum, y_ref, 0.f), theirs = other_ml[r];
+        Part ends;
+#pragma unroll 1
+        for (int i = 0; i < DH; i += 32) {
+          uint32_t v[32];
+          umma::ld32(to + i, v);
+          umma::ld_wait();
+#pragma unroll
+          for (int u = 0; u < 32; u += 4) {
+            if (!live) break;
+            const float4 x = reinterpret_cast<const float4 *>(other)[((i + u) / 4) * M + r];
+            const float4 y = make_float4(__uint_as_float(v[u]), __uint_as_float(v[u + 1]), __uint_as_float(v[u + 2]),
+                                         __uint_as_float(v[u + 3]));
+            ends = join_parts<2>(2, [&](int k) { return k ? theirs : mine; }, [&](int k) { return k ? x : y; });
+            if (Z == 1)
+              store_row(a, ends, orow, DH, i + u);
+            else
+              *reinterpret_cast<float4 *>(split.o + prow * DH + i + u) = ends.v;
+          }
+          __syncwarp();
+        }
+        if (live && Z > 1) split.ml[prow] = make_float4(ends.M, ends.l, ends.Y, 0.f);
+      }
       umma::fence_before();
     }
     __syncthreads();
     umma::fence_after();
     gave_up = *abort != 0;
-    if (LIST || gave_up) break;
     tile_i += gridDim.x;
+    if (LIST || gave_up || tile_i >= t.total) break;
     t = find_tile<256>(a, per, tile_i);
-    if (t.n == 0) break;
     if (tid == 0) {
-      for (int i = 0; i < MAX_STAGES; ++i) {
+      for (int i = 0; i < MAX_STAGES; ++i)
         mbar_inval(&sh.kfull[i]), mbar_inval(&sh.vfull[i]), mbar_inval(&sh.kempty[i]), mbar_inval(&sh.vempty[i]);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_inval(&sh.sfull[i]), mbar_inval(&sh.pvdone[i]), mbar_inval(&sh.sfree[i]), mbar_inval(&sh.pfull[i]);
-      }
-      mbar_inval(&sh.done), mbar_inval(&sh.placed[0]), mbar_inval(&sh.placed[1]), mbar_inval(&sh.scan);
+      for (int i = 0; i < 4; ++i) mbar_inval(&sh.sfull[i]), mbar_inval(&sh.pfull[i]);
+      for (int i = 0; i < 2; ++i) mbar_inval(&sh.pvdone[i]), mbar_inval(&sh.placed[i]), mbar_inval(&sh.scan[i]);
+      mbar_inval(&sh.done), mbar_inval(&sh.joined);
     }
     __syncthreads();
   }
