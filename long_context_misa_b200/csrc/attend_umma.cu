@@ -5,10 +5,11 @@
 //
 // A CTA holds up to 128 rows (lanes of tensor memory) of one key/value head
 // and a share of the tokens, in chunks of 64:
-//   4 producer warps   gather a chunk's keys (2 warps) and values (2) into
-//                      rings of 128-byte-swizzled tiles: cp.async for bf16
-//                      rows; e4m3 rows go through a ring of their own and are
-//                      widened to f16 by the threads that brought them
+//   4 producer warps   bring a chunk's keys (2 warps) and values (2) into
+//                      rings of 128-byte-swizzled tiles: TMA for stretches of
+//                      a prefix, cp.async for listed and drafted tokens.
+//                      e4m3 rows go through a ring of their own and are
+//                      widened to f16 there
 //   1 MMA thread       S_j = Q K_j^T, two chunks ahead of O += P_j V_j (V as
 //                      the MN-major operand, P from tensor memory)
 //   2 x 4 softmax warps, one row per thread: the even and the odd chunks, each
@@ -19,8 +20,9 @@
 // Tensor memory: two O of 128 columns, four S (then P) of 64.
 // A chunk (32 KB of bf16 rows) is 512 cycles of MMA at M = 128 and 1425 of the
 // SM's share of HBM; a softmax warp needs about 1500 cycles for it (mostly
-// latencies), which one set of warps could not hide (measured: 24 queries x 4
-// heads over 32K bf16 tokens of 4 sequences: 163 us with one set).
+// latencies), and a proxy fence of the MMA thread per operand tile, which rows
+// brought by cp.async need, 300 (measured, 24 queries x 4 heads over 32K bf16
+// tokens of 4 sequences: 163 us with one set and cp.async, 143 with two).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -58,6 +60,7 @@ constexpr int MAX_STAGES = 10;
 
 struct Shared {
   uint64_t kfull[MAX_STAGES], kempty[MAX_STAGES], vfull[MAX_STAGES], vempty[MAX_STAGES];
+  uint64_t rawfull[2][8], rawempty[2][8];
   uint64_t sfull[4], pfull[4], pvdone[2], done;
   uint64_t placed[2], scan[2], joined;  // meetings of a producer group, a softmax set, both sets
   uint32_t tmem_base;
@@ -139,7 +142,9 @@ __device__ __forceinline__ uint32_t tile_at(int r, int pc, int blk) {
 }
 
 template <class F, bool LIST>
-__global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, AttendView a, Split split, int per) {
+__global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, AttendView a, Split split, int per,
+                                                               const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap, int tma) {
   grid_dep_sync();
   constexpr int DH = F::DH, NK = F::NK, NV = F::NV, BLK = F::BLK, TILE = F::TILE, CPR = F::CPR, PER = F::PER;
   constexpr bool FP8 = F::FP8;
@@ -177,6 +182,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_init(&sh.kfull[i], GROUP), mbar_init(&sh.vfull[i], FP8 ? GROUP : GROUP + W);
         mbar_init(&sh.kempty[i], 1), mbar_init(&sh.vempty[i], 1);  // the MMAs' commit
       }
+      for (int i = 0; i < 8; ++i)
+        for (int v = 0; v < 2; ++v) mbar_init(&sh.rawfull[v][i], 1), mbar_init(&sh.rawempty[v][i], GROUP);
       for (int i = 0; i < 4; ++i) mbar_init(&sh.sfull[i], 1), mbar_init(&sh.pfull[i], 128);  // a softmax set
       for (int i = 0; i < 2; ++i)
         mbar_init(&sh.pvdone[i], 1), mbar_init(&sh.placed[i], GROUP), mbar_init(&sh.scan[i], 128);
@@ -186,22 +193,23 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
     }
     __syncthreads();
     if (tid < M) {
+      const int r = tid;
       int s = -1, len = 0;
-      if (tid < n_rows) {
-        len = attend_prefix(c, a, row_query(tid), &s);
+      if (r < n_rows) {
+        len = attend_prefix(c, a, row_query(r), &s);
         if (s >= 0) {
           sh.seq = s;  // the same in every row that has one
           atomicMax(&sh.max_len, len);
         }
         atomicMin(&sh.min_len, s >= 0 ? len : -1);
       }
-      sh.len[tid] = s >= 0 ? len : -1;
-      sh.query[tid] = tid < n_rows ? row_query(tid) : -1;
+      sh.len[r] = s >= 0 ? len : -1;
+      sh.query[r] = r < n_rows ? row_query(r) : -1;
     }
     // ---- Q: 16-bit rows, K-major with 128-byte swizzle; e4m3 caches: f16
     // after a power of two per row.  DH / 8 lanes hold a row ----
-    constexpr int QL = DH / 8;
-    for (int e = tid; e < (M * QL + THREADS - 1) / THREADS * THREADS; e += THREADS) {
+    constexpr int QL = DH / 8, QT = THREADS - M;  // (the other threads look up the rows meanwhile)
+    for (int e = tid - M; tid >= M && e < (M * QL + QT - 1) / QT * QT; e += QT) {
       const int r = min(e / QL, M - 1), p = e % QL;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (e < M * QL && r < n_rows)
@@ -302,6 +310,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       // whether chunk j is a stretch of the prefix: its rows need no list, and
       // no meeting of the group to share one
       auto stretch = [&](int j) { return !LIST && cb + j < c1; };
+      // ... and TMA brings it, what lies behind the prefix included (nobody
+      // sees it, and what is not finite there is taken out with the masked)
+      auto by_tma = [&](int j) { return tma && stretch(j); };
+      const CUtensorMap *map = vals ? &vmap : &kmap;
       const uint8_t *lane0 = base + ((int64_t)r0 * c.H_kv + hk) * (CPR * 16) + pc * 16;
       const int64_t step = (int64_t)RSTEP * c.H_kv * (CPR * 16);
       // this thread's pieces of chunk j: rows r0, r0 + RSTEP, ... to at(i, row)
@@ -340,8 +352,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           if (j >= nst && !wait_bar(&empty[st], wrap, abort, c)) break;
           if (!place(j, row)) break;
           const uint32_t dst = smem_addr(ring + st * TILE);
-          copy(j, [&](int, int r) { return dst + tile_at(r, pc, BLK); });
-          cp_async_arrive(&full[st]);
+          if (by_tma(j)) {
+            if (pt == 0) {
+              mbar_arrive_expect_tx(&full[st], TILE);
+#pragma unroll
+              for (int b = 0; b < DH / 64; ++b)
+                umma::tma_load_3d(dst + b * BLK, map, 64 * b, hk, seq * c.L_cap + (cb + j) * TOK, &full[st]);
+            } else {
+              mbar_arrive(&full[st]);
+            }
+          } else {
+            copy(j, [&](int, int r) { return dst + tile_at(r, pc, BLK); });
+            cp_async_arrive(&full[st]);
+          }
           if (notes) mbar_arrive(&full[st]);
           advance();
         }
@@ -356,8 +379,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           tok = listed(j + 1);
           if (j < n) {
             if (!place(j, row)) return false;
-            const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW) + pt * 16;
-            copy(j, [&](int i, int) { return dst + i * (GROUP * 16); });
+            const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW);
+            if (by_tma(j)) {
+              if (pt == 0) {
+                if (j >= NR && !wait_bar(&sh.rawempty[vals][j % NR], ((j / NR) & 1) ^ 1, abort, c)) return false;
+                mbar_arrive_expect_tx(&sh.rawfull[vals][j % NR], F::RAW);
+                umma::tma_load_3d(dst, map, 0, hk, seq * c.L_cap + (cb + j) * TOK, &sh.rawfull[vals][j % NR]);
+              }
+            } else {
+              copy(j, [&](int i, int) { return dst + (i * GROUP + pt) * 16; });
+            }
           }
           cp_async_commit();
           return true;
@@ -367,6 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         for (int j = 0; j < n && ok; ++j) {
           if (!(ok = bring(j + NR - 1))) break;
           cp_async_wait<NR - 1>();
+          if (by_tma(j) && !(ok = wait_bar(&sh.rawfull[vals][j % NR], (j / NR) & 1, abort, c))) break;
           if (j >= nst && !(ok = wait_bar(&empty[st], wrap, abort, c))) break;
           const uint8_t *from = raw + (j % NR) * F::RAW + pt * 16;
           uint8_t *dst = ring + st * TILE;
@@ -379,6 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc, BLK)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc + 1, BLK)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
+          mbar_arrive(&sh.rawempty[vals][j % NR]);
           umma::fence_proxy_async();
           mbar_arrive(&full[st]);
           advance();
@@ -392,38 +425,46 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         constexpr uint32_t IDS = (1u << 4) | (FMT << 7) | (FMT << 10) | ((uint32_t)(TOK >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
         constexpr uint32_t IDO = (1u << 4) | (FMT << 7) | (FMT << 10) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) |
                                  ((uint32_t)(M >> 4) << 24);
-        const uint32_t qa = smem_addr(q_s);
         bool ok = true;
+        // Descriptors differ in their low words only (addresses in 16 bytes):
+        // the thread's own instructions are the loop's length, so they are
+        // kept to an add per product and counters instead of divisions.
+        const uint64_t kd0 = umma::smem_desc_sw128(smem_addr(k_s)), qd = umma::smem_desc_sw128(smem_addr(q_s));
+        const uint64_t vd0 = desc_mn(smem_addr(v_s), BLK);
+        uint32_t kst = 0, kph = 0, vst = 0, vph = 0;
+        // rows that cp.async brought become visible to the tensor cores here;
+        // TMA's are, and widened ones were made so by who wrote them
+        auto fence = [&](int j) {
+          if (!FP8 && !(tma && !LIST && cb + j < c1)) umma::fence_proxy_async();
+          umma::fence_after();
+        };
         auto s_of = [&](int j) {
-          const int st = j % NK;
           // the columns held P_(j-4)
           if (j >= 4) ok = ok && wait_bar(&sh.pvdone[j & 1], ((j - 4) >> 1) & 1, abort, c);
-          ok = ok && wait_bar(&sh.kfull[st], (j / NK) & 1, abort, c);
+          ok = ok && wait_bar(&sh.kfull[kst], kph, abort, c);
           if (!ok) return;
-          umma::fence_proxy_async();
-          umma::fence_after();
-          const uint32_t ka = smem_addr(k_s + st * TILE);
+          fence(j);
+          const uint64_t kd = kd0 + kst * (TILE >> 4);
+          const uint32_t to = tmem + T_S + (j & 3) * TOK;
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t at = (kk & 3) * 32;
-            umma::mma<false>(tmem + T_S + (j & 3) * TOK, umma::smem_desc_sw128(qa + (kk >> 2) * F::QBLK + at),
-                             umma::smem_desc_sw128(ka + (kk >> 2) * BLK + at), IDS, kk ? 1u : 0u);
-          }
-          umma::commit(&sh.kempty[st]);
+          for (int kk = 0; kk < DH / 16; ++kk)
+            umma::mma<false>(to, qd + (((kk >> 2) * F::QBLK + (kk & 3) * 32) >> 4),
+                             kd + (((kk >> 2) * BLK + (kk & 3) * 32) >> 4), IDS, kk ? 1u : 0u);
+          umma::commit(&sh.kempty[kst]);
           umma::commit(&sh.sfull[j & 3]);
+          if (++kst == NK) kst = 0, kph ^= 1;
         };
         auto pv = [&](int j) {
-          const int st = j % NV;
-          ok = ok && wait_bar(&sh.vfull[st], (j / NV) & 1, abort, c) && wait_bar(&sh.pfull[j & 3], (j >> 2) & 1, abort, c);
+          ok = ok && wait_bar(&sh.vfull[vst], vph, abort, c) && wait_bar(&sh.pfull[j & 3], (j >> 2) & 1, abort, c);
           if (!ok) return;
-          umma::fence_proxy_async();
-          umma::fence_after();
-          const uint32_t va = smem_addr(v_s + st * TILE);
+          fence(j);
+          const uint64_t vd = vd0 + vst * (TILE >> 4);
+          const uint32_t to = tmem + T_O + (j & 1) * 128, from = tmem + T_S + (j & 3) * TOK;
 #pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk)
-            mma_ts(tmem + T_O + (j & 1) * 128, tmem + T_S + (j & 3) * TOK + kk * 8, desc_mn(va + kk * 2048, BLK), IDO);
-          umma::commit(&sh.vempty[st]);
+          for (int kk = 0; kk < TOK / 16; ++kk) mma_ts(to, from + kk * 8, vd + ((kk * 2048) >> 4), IDO);
+          umma::commit(&sh.vempty[vst]);
           umma::commit(&sh.pvdone[j & 1]);
+          if (++vst == NV) vst = 0, vph ^= 1;
         };
         s_of(0);
         if (n > 1) s_of(1);
@@ -691,6 +732,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       }
       umma::fence_before();
     }
+    // what was written to the rings' memory here comes before the next tile's
+    // TMA; where a wait ran out, copies may still be on their way: they land
+    // well within a millisecond
+    umma::fence_proxy_async();
+    if (*abort)
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
+      }
     __syncthreads();
     umma::fence_after();
     gave_up = *abort != 0;
@@ -700,6 +748,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
     if (tid == 0) {
       for (int i = 0; i < MAX_STAGES; ++i)
         mbar_inval(&sh.kfull[i]), mbar_inval(&sh.vfull[i]), mbar_inval(&sh.kempty[i]), mbar_inval(&sh.vempty[i]);
+      for (int i = 0; i < 8; ++i)
+        for (int v = 0; v < 2; ++v) mbar_inval(&sh.rawfull[v][i]), mbar_inval(&sh.rawempty[v][i]);
       for (int i = 0; i < 4; ++i) mbar_inval(&sh.sfull[i]), mbar_inval(&sh.pfull[i]);
       for (int i = 0; i < 2; ++i) mbar_inval(&sh.pvdone[i]), mbar_inval(&sh.placed[i]), mbar_inval(&sh.scan[i]);
       mbar_inval(&sh.done), mbar_inval(&sh.joined);
@@ -715,8 +765,13 @@ cudaError_t run(const KvView &c, const AttendView &a, const Split &sp, int per, 
   struct Tag {};
   const int have = cached_per_device<Tag>([] { return opt_in_max_dyn_smem(attend_umma_kernel<F, LIST>); });
   if (have < F::SMEM) return cudaErrorInvalidConfiguration;
+  CUtensorMap km = {}, vm = {};
+  const unsigned long long tokens = (unsigned long long)c.n_seq * c.L_cap;
+  const int tma = !LIST && tokens < 0x7fffff00ull &&
+                  umma::make_map_heads(&km, c.k, F::FP8, F::DH, c.H_kv, tokens, F::FP8 ? F::DH : 64, TOK, !F::FP8) &&
+                  umma::make_map_heads(&vm, c.v, F::FP8, F::DH, c.H_kv, tokens, F::FP8 ? F::DH : 64, TOK, !F::FP8);
   return launch_kernel(attend_umma_kernel<F, LIST>, dim3((unsigned)tiles, c.H_kv, sp.Z), dim3(THREADS), F::SMEM, s, c, a,
-                       sp, per);
+                       sp, per, km, vm, tma);
 }
 
 }  // namespace

@@ -534,5 +534,20 @@ bool make_map_f32_rows(CUtensorMap *map, const float *base, unsigned long long c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_heads(CUtensorMap *map, const void *base, bool u8, int d, int heads, unsigned long long tokens, int box_x,
+                    int box_tokens, bool swizzle) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)d * (u8 ? 1 : 2);
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {row, row * heads};
+  const cuuint32_t box[3] = {(cuuint32_t)box_x, 1, (cuuint32_t)box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace umma
 }  // namespace misa

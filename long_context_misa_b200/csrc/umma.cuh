@@ -67,6 +67,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
 // TMA tile store from shared memory (bulk-group completion): box of the map at
 // element coordinates (x, y); elements outside the tensor are not written.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
@@ -111,6 +118,11 @@ bool make_map_2d(CUtensorMap *map, const void *base, bool u8, unsigned long long
 // the base or the row pitch is not 16-byte aligned.
 bool make_map_f32_rows(CUtensorMap *map, const float *base, unsigned long long cols, unsigned long long rows,
                        unsigned long long ld, int box_x, int box_rows);
+// Host: a 3-D map of [tokens][heads][d] rows (bf16, or bytes when u8), boxes of
+// box_x elements of one head of box_tokens tokens, with 128-byte swizzle or
+// none; false if unavailable.
+bool make_map_heads(CUtensorMap *map, const void *base, bool u8, int d, int heads, unsigned long long tokens, int box_x,
+                    int box_tokens, bool swizzle);
 bool encoder_available();
 
 }  // namespace umma
