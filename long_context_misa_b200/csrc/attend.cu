@@ -706,15 +706,15 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
     p.nr = 0, p.row_tiles = 1, p.cluster = false;
     p.per = list ? 1 : 128 / G;
     p.tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
-    const int chunks = cdiv(list ? k : c.L_cap, 64) + cdiv(n_draft, 64);
+    const int chunks = cdiv(list ? k : c.L_cap, 128) + cdiv(n_draft, 128);
     const int64_t units = (int64_t)p.tiles * c.H_kv;
     // shares: the fewest chunk times over the waves of one CTA per SM, with
-    // about 12 chunks' time for a CTA's beginning and end
+    // about 8 chunks' time for a CTA's beginning and end
     const int sms = device_sms();
     p.Z = 1;
     int64_t best = INT64_MAX;
     for (int z = 1; z <= std::min(chunks, 32); ++z) {
-      const int64_t t = (units * z + sms - 1) / sms * (cdiv(chunks, z) + 12);
+      const int64_t t = (units * z + sms - 1) / sms * (cdiv(chunks, z) + 8);
       if (t < best) best = t, p.Z = z;
     }
     return p;

@@ -4,25 +4,25 @@
 // numbers as attend.cu.
 //
 // A CTA holds up to 128 rows (lanes of tensor memory) of one key/value head
-// and a share of the tokens, in chunks of 64:
+// and a share of the tokens, in chunks of 128:
 //   4 producer warps   bring a chunk's keys (2 warps) and values (2) into
 //                      rings of 128-byte-swizzled tiles: TMA for stretches of
 //                      a prefix, cp.async for listed and drafted tokens.
 //                      e4m3 rows go through a ring of their own and are
 //                      widened to f16 there
-//   1 MMA thread       S_j = Q K_j^T, two chunks ahead of O += P_j V_j (V as
-//                      the MN-major operand, P from tensor memory)
-//   2 x 4 softmax warps, one row per thread: the even and the odd chunks, each
-//                      with its own O and running maximum, so that neither
-//                      waits for the other; they join at the end.  Weights go
-//                      back into the columns of S; O is touched only when a
-//                      weight passes 256 times its reference.
-// Tensor memory: two O of 128 columns, four S (then P) of 64.
-// A chunk (32 KB of bf16 rows) is 512 cycles of MMA at M = 128 and 1425 of the
-// SM's share of HBM; a softmax warp needs about 1500 cycles for it (mostly
-// latencies), and a proxy fence of the MMA thread per operand tile, which rows
-// brought by cp.async need, 300 (measured, 24 queries x 4 heads over 32K bf16
-// tokens of 4 sequences: 163 us with one set and cp.async, 143 with two).
+//   1 MMA thread       S_j = Q K_j^T, a chunk ahead of O += P_j V_j (V as the
+//                      MN-major operand, P from tensor memory)
+//   2 x 4 softmax warps, one row per thread: a set takes half of a chunk's
+//                      tokens, with its own O and running maximum, so that
+//                      neither waits for the other; they join at the end.
+//                      Weights go back into the columns of S; O is touched
+//                      only when a weight passes 256 times its reference.
+// Tensor memory: two O of 128 columns, two S (then P) of 128.
+// A chunk (64 KB of bf16 rows) is 1024 cycles of MMA at M = 128 and 2850 of
+// the SM's share of HBM.  What decides is the MMA thread: an instruction costs
+// it 65 to 85 cycles, a commit or a wait 70, so S is issued at N = 128 for
+// both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences: 143 us
+// with chunks of 64).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -31,13 +31,13 @@
 namespace misa {
 namespace {
 
-constexpr int M = 128, TOK = 64;  // rows and tokens of a tile
-constexpr int W = TOK / 32;        // mask words of a tile
+constexpr int M = 128, TOK = 128, HALF = 64;  // rows and tokens of a tile, a set's tokens
+constexpr int W = HALF / 32;                  // mask words of a half
 constexpr int WARPS = 13, THREADS = WARPS * 32;
 constexpr int PROD0 = 8, MMA_WARP = 12;  // warps 0..7 softmax, 8 and 9 keys, 10 and 11 values
 constexpr int GROUP = 64;                // threads of a producer group
-constexpr int SLOTS = 32;                // masks and scales in flight (more than the rings can be ahead)
-constexpr int T_O = 0, T_S = 256, T_COLS = 512;  // O of set g at 128 g, S of chunk j at 256 + 64 (j & 3)
+constexpr int SLOTS = 16;                // masks and scales in flight (more than the rings can be ahead)
+constexpr int T_O = 0, T_S = 256, T_COLS = 512;  // O of set g at 128 g, S of chunk j at 256 + 128 (j & 1)
 constexpr int BAD = 128;  // non-finite values handled per round
 
 template <int DH_, bool FP8_>
@@ -51,22 +51,23 @@ struct UCfg {
   static constexpr int PER = TOK * CPR / GROUP;        // of them per producer thread and tile
   static constexpr int RAW = FP8 ? TOK * DH : 0;       // a tile of codes
   // ring stages: operand tiles of keys and values, tiles of codes of either
-  static constexpr int NK = FP8 ? 3 : DH > 64 ? 4 : 8, NV = FP8 ? 3 : DH > 64 ? 6 : 10, NR = FP8 ? (DH > 64 ? 4 : 8) : 0;
+  static constexpr int NK = FP8 ? (DH > 64 ? 1 : 2) : DH > 64 ? 2 : 4, NV = FP8 ? (DH > 64 ? 2 : 3) : DH > 64 ? 3 : 5;
+  static constexpr int NR = FP8 ? (DH > 64 ? 2 : 4) : 0;
   static constexpr int SMEM = QTILE + (NK + NV) * TILE + 2 * NR * RAW + 1024;
   static_assert((NK + NV) * TILE >= M * (DH * 4 + 16), "the odd set's result takes the rings' place");
-  static_assert(GROUP == TOK && NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
+  static_assert(2 * GROUP == TOK && NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
 };
-constexpr int MAX_STAGES = 10;
+constexpr int MAX_STAGES = 5;
 
 struct Shared {
   uint64_t kfull[MAX_STAGES], kempty[MAX_STAGES], vfull[MAX_STAGES], vempty[MAX_STAGES];
   uint64_t rawfull[2][8], rawempty[2][8];
-  uint64_t sfull[4], pfull[4], pvdone[2], done;
+  uint64_t sfull[2], pfull[2][2], pvdone[2], done;  // pfull[set][turn], pvdone[set]
   uint64_t placed[2], scan[2], joined;  // meetings of a producer group, a softmax set, both sets
   uint32_t tmem_base;
   int abort;
   int row_idx[2][2][TOK];   // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
-  uint32_t have[SLOTS][W];  // which tokens of a chunk are there
+  uint32_t have[SLOTS][2 * W];  // which tokens of a chunk are there
   int len[M], query[M];
   float mul[M];  // scale log2(e), over the row's power of two (e4m3 caches)
   int seq, max_len, min_len;
@@ -179,12 +180,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       for (int i = 0; i < MAX_STAGES; ++i) {
         // every producer thread of the group (bf16: as its copies land, and
         // the lanes that noted the masks)
-        mbar_init(&sh.kfull[i], GROUP), mbar_init(&sh.vfull[i], FP8 ? GROUP : GROUP + W);
+        mbar_init(&sh.kfull[i], GROUP), mbar_init(&sh.vfull[i], FP8 ? GROUP : GROUP + 2);
         mbar_init(&sh.kempty[i], 1), mbar_init(&sh.vempty[i], 1);  // the MMAs' commit
       }
       for (int i = 0; i < 8; ++i)
         for (int v = 0; v < 2; ++v) mbar_init(&sh.rawfull[v][i], 1), mbar_init(&sh.rawempty[v][i], GROUP);
-      for (int i = 0; i < 4; ++i) mbar_init(&sh.sfull[i], 1), mbar_init(&sh.pfull[i], 128);  // a softmax set
+      for (int i = 0; i < 2; ++i)
+        mbar_init(&sh.sfull[i], 1), mbar_init(&sh.pfull[0][i], 128), mbar_init(&sh.pfull[1][i], 128);  // a softmax set
       for (int i = 0; i < 2; ++i)
         mbar_init(&sh.pvdone[i], 1), mbar_init(&sh.placed[i], GROUP), mbar_init(&sh.scan[i], 128);
       mbar_init(&sh.done, 1), mbar_init(&sh.joined, 256);
@@ -260,17 +262,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       const int64_t srow = (int64_t)max(seq, 0) * c.L_cap * c.H_kv;
       uint8_t *ring = vals ? v_s : k_s;
       const int nst = vals ? NV : NK;
-      auto listed = [&](int j) -> int {  // token pt of chunk j as listed
-        const int i = (cb + j) * TOK + pt;
+      // this thread's tokens of a chunk: pt and pt + GROUP (h = 0, 1)
+      auto listed = [&](int j, int h) -> int {  // as listed
+        const int i = (cb + j) * TOK + pt + h * GROUP;
         if (!LIST) return i;
         return j < n && i < a.k ? __ldg(a.topk + (int64_t)t.q0 * a.k + i) : -1;
       };
-      auto row_of = [&](int j, int tok) -> int {
+      auto row_of = [&](int j, int h, int tok) -> int {
         if (j >= n) return -1;
         if (cb + j < c1) {
           if (tok < 0 || tok >= max_len) return -1;
         } else {
-          const int d = (cb + j - c1) * TOK + pt;
+          const int d = (cb + j - c1) * TOK + pt + h * GROUP;
           if (d >= n_draft) return -1;
           if (LIST && !((a.draft_mask[(int64_t)t.q0 * words + (d >> 5)] >> (d & 31)) & 1u)) return -1;
           const int64_t p = (int64_t)draft0 + d;
@@ -282,26 +285,38 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         }
         return tok * c.H_kv + hk;
       };
+      int ahead[2] = {listed(0, 0), listed(0, 1)};  // chunk j's tokens, read a chunk before
       // rows of chunk j into row_idx[..][j & 1]; the values' group also notes
       // which are there and (e4m3) brings the scales, for the softmax warps,
       // who wait for the values' tile
       const bool notes = vals && lane == 0;
       int meetings = 0;
-      auto bring_scale = [&](int j, int row) {
-        cp_async4(smem_addr(&scales.k[j & (SLOTS - 1)][pt]), c.k_scale + srow + max(row, 0), row >= 0);
-        cp_async4(smem_addr(&scales.v[j & (SLOTS - 1)][pt]), c.v_scale + srow + max(row, 0), row >= 0);
-      };
-      auto place = [&](int j, int row) -> bool {
+      auto place = [&](int j) -> bool {
+        const int rows[2] = {row_of(j, 0, ahead[0]), row_of(j, 1, ahead[1])};
+        ahead[0] = listed(j + 1, 0), ahead[1] = listed(j + 1, 1);
+        if (FP8 && vals) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t row = srow + max(rows[h], 0);
+            cp_async4(smem_addr(&scales.k[j & (SLOTS - 1)][pt + h * GROUP]), c.k_scale + row, rows[h] >= 0);
+            cp_async4(smem_addr(&scales.v[j & (SLOTS - 1)][pt + h * GROUP]), c.v_scale + row, rows[h] >= 0);
+          }
+        }
         if (!LIST && cb + j < c1) {
-          const int left = max_len - (cb + j) * TOK - pt;  // (pt is 0 or 32 where it notes)
-          if (notes) sh.have[j & (SLOTS - 1)][pt >> 5] = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
-          if (FP8 && vals) bring_scale(j, row);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int left = max_len - (cb + j) * TOK - pt - h * GROUP;  // (pt is 0 or 32 where it notes)
+            if (notes)
+              sh.have[j & (SLOTS - 1)][(pt >> 5) + 2 * h] = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+          }
           return true;
         }
-        sh.row_idx[vals][j & 1][pt] = row;
-        const uint32_t b = __ballot_sync(0xffffffffu, row >= 0);
-        if (notes) sh.have[j & (SLOTS - 1)][pt >> 5] = b;
-        if (FP8 && vals) bring_scale(j, row);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sh.row_idx[vals][j & 1][pt + h * GROUP] = rows[h];
+          const uint32_t b = __ballot_sync(0xffffffffu, rows[h] >= 0);
+          if (notes) sh.have[j & (SLOTS - 1)][(pt >> 5) + 2 * h] = b;
+        }
         mbar_arrive(&sh.placed[vals]);
         return wait_bar(&sh.placed[vals], meetings++ & 1, abort, c);
       };
@@ -322,10 +337,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           const int t0 = (cb + j) * TOK, left = max_len - t0;
           const uint8_t *p = lane0 + (int64_t)t0 * c.H_kv * (CPR * 16);
           if (left >= TOK) {
-#pragma unroll
+#pragma unroll 8
             for (int i = 0; i < PER; ++i, p += step) cp_async16(at(i, r0 + i * RSTEP), p);
           } else {
-#pragma unroll
+#pragma unroll 8
             for (int i = 0; i < PER; ++i, p += step) {
               const bool there = r0 + i * RSTEP < left;
               cp_async16(at(i, r0 + i * RSTEP), there ? p : base, there);
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           return;
         }
         const int *idx = sh.row_idx[vals][j & 1];
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < PER; ++i) {
           const int r = r0 + i * RSTEP, x = idx[r];
           cp_async16(at(i, r), base + (uint64_t)(uint32_t)max(x, 0) * (CPR * 16) + pc * 16, x >= 0);
@@ -345,12 +360,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         if (++st == nst) st = 0, wrap ^= 1;
       };
       if (!FP8) {
-        int tok = listed(0);
         for (int j = 0; j < n; ++j) {
-          const int row = row_of(j, tok);
-          tok = listed(j + 1);
           if (j >= nst && !wait_bar(&empty[st], wrap, abort, c)) break;
-          if (!place(j, row)) break;
+          if (!place(j)) break;
           const uint32_t dst = smem_addr(ring + st * TILE);
           if (by_tma(j)) {
             if (pt == 0) {
@@ -373,12 +385,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         // codes: NR tiles on their way, each thread its own pieces
         constexpr int NR = F::NR;
         uint8_t *raw = raw_s + (vals ? NR * F::RAW : 0);
-        int tok = listed(0);
         auto bring = [&](int j) -> bool {
-          const int row = row_of(j, tok);
-          tok = listed(j + 1);
           if (j < n) {
-            if (!place(j, row)) return false;
+            if (!place(j)) return false;
             const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW);
             if (by_tma(j)) {
               if (pt == 0) {
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           if (j >= nst && !(ok = wait_bar(&empty[st], wrap, abort, c))) break;
           const uint8_t *from = raw + (j % NR) * F::RAW + pt * 16;
           uint8_t *dst = ring + st * TILE;
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < PER; ++i) {
             const uint4 v = *reinterpret_cast<const uint4 *>(from + i * (GROUP * 16));
             const int r = r0 + i * RSTEP;
@@ -439,37 +448,42 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           umma::fence_after();
         };
         auto s_of = [&](int j) {
-          // the columns held P_(j-4)
-          if (j >= 4) ok = ok && wait_bar(&sh.pvdone[j & 1], ((j - 4) >> 1) & 1, abort, c);
+          // the columns held P_(j-2); set 1's products are the later ones
+          if (j >= 2) ok = ok && wait_bar(&sh.pvdone[1], j & 1, abort, c);
           ok = ok && wait_bar(&sh.kfull[kst], kph, abort, c);
           if (!ok) return;
           fence(j);
           const uint64_t kd = kd0 + kst * (TILE >> 4);
-          const uint32_t to = tmem + T_S + (j & 3) * TOK;
+          const uint32_t to = tmem + T_S + (j & 1) * TOK;
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk)
             umma::mma<false>(to, qd + (((kk >> 2) * F::QBLK + (kk & 3) * 32) >> 4),
                              kd + (((kk >> 2) * BLK + (kk & 3) * 32) >> 4), IDS, kk ? 1u : 0u);
           umma::commit(&sh.kempty[kst]);
-          umma::commit(&sh.sfull[j & 3]);
+          umma::commit(&sh.sfull[j & 1]);
           if (++kst == NK) kst = 0, kph ^= 1;
         };
         auto pv = [&](int j) {
-          ok = ok && wait_bar(&sh.vfull[vst], vph, abort, c) && wait_bar(&sh.pfull[j & 3], (j >> 2) & 1, abort, c);
+          ok = ok && wait_bar(&sh.vfull[vst], vph, abort, c);
           if (!ok) return;
           fence(j);
-          const uint64_t vd = vd0 + vst * (TILE >> 4);
-          const uint32_t to = tmem + T_O + (j & 1) * 128, from = tmem + T_S + (j & 3) * TOK;
 #pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk) mma_ts(to, from + kk * 8, vd + ((kk * 2048) >> 4), IDO);
+          for (int g = 0; g < 2; ++g) {
+            ok = ok && wait_bar(&sh.pfull[g][j & 1], (j >> 1) & 1, abort, c);
+            if (!ok) return;
+            umma::fence_after();
+            const uint64_t vd = vd0 + ((vst * TILE + g * HALF * 128) >> 4);
+            const uint32_t to = tmem + T_O + g * 128, from = tmem + T_S + (j & 1) * TOK + g * HALF;
+#pragma unroll
+            for (int kk = 0; kk < HALF / 16; ++kk) mma_ts(to, from + kk * 8, vd + ((kk * 2048) >> 4), IDO);
+            umma::commit(&sh.pvdone[g]);
+          }
           umma::commit(&sh.vempty[vst]);
-          umma::commit(&sh.pvdone[j & 1]);
           if (++vst == NV) vst = 0, vph ^= 1;
         };
         s_of(0);
-        if (n > 1) s_of(1);
         for (int j = 0; j < n && ok; ++j) {
-          if (j + 2 < n) s_of(j + 2);
+          if (j + 1 < n) s_of(j + 1);
           pv(j);
         }
         // nothing in flight past here (bounded)
@@ -477,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_wait(&sh.done, 0);
       }
     } else {
-      // ---- softmax: row tid % 128, chunks g, g + 2, ... ----
+      // ---- softmax: row tid % 128, half g of every chunk ----
       const int g = warp >> 2, r = tid & 127;
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = tl + T_O + g * 128;
       const int my_len = sh.len[r], my_query = sh.query[r];
@@ -497,9 +511,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         for (int i = 0; i < DH; i += 16) st16(to + i, zero);
         st_wait();
       }
-      for (int j = g; j < n && ok; j += 2) {
+      for (int j = 0; j < n && ok; ++j) {
         const int slot = j & (SLOTS - 1), ck = cb + j;
-        ok = wait(&sh.sfull[j & 3], (j >> 2) & 1);
+        ok = wait(&sh.sfull[j & 1], (j >> 1) & 1);
         // the masks and scales come with the chunk's values (whose stage is
         // not filled again before this chunk is done); a stretch of the prefix
         // needs no mask from there
@@ -511,19 +525,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         uint32_t see[W];
         bool masked = false;
         if (stretch) {
-          const int left = (r < n_rows ? my_len : max_len) - ck * TOK;
+          const int left = (r < n_rows ? my_len : max_len) - ck * TOK - g * HALF;
           see[0] = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
           see[1] = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1u : 0u;
-          masked = left < TOK;
+          masked = left < HALF;
         } else {
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            uint32_t v = sh.have[slot][w];
+            uint32_t v = sh.have[slot][W * g + w];
             if (!LIST && r < n_rows) {  // (nobody reads the other rows)
               if (my_len < 0) {
                 v = 0u;
               } else {
-                const int d0 = (ck - c1) * TOK + w * 32;
+                const int d0 = (ck - c1) * TOK + g * HALF + w * 32;
                 uint32_t m = d0 < n_draft ? a.draft_mask[(int64_t)my_query * words + (d0 >> 5)] : 0u;
                 if (n_draft - d0 < 32) m &= n_draft > d0 ? (1u << (n_draft - d0)) - 1u : 0u;
                 if (m & ~v) flag(c, MISA_DEV_BAD_POSITION);
@@ -535,10 +549,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           }
         }
         masked = __any_sync(0xffffffffu, masked);
-        const uint32_t ts = tl + T_S + (j & 3) * TOK;
-        const float *ks = scales.k[FP8 ? slot : 0], *vs = scales.v[FP8 ? slot : 0];
+        const uint32_t ts = tl + T_S + (j & 1) * TOK + g * HALF;
+        const float *ks = scales.k[FP8 ? slot : 0] + g * HALF, *vs = scales.v[FP8 ? slot : 0] + g * HALF;
 
-        uint32_t pk[TOK / 2];  // P as it goes back to tensor memory
+        uint32_t pk[HALF / 2];  // P as it goes back to tensor memory
         auto weigh = [&](auto mk, float &sum) -> float {
           float top = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t v[W][32];
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           return top;
         };
         float sum = 0.f, top = LAZY + 1.f;
-        if (j > g) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
+        if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
         if (__any_sync(0xffffffffu, top > LAZY)) {
           float mx = NEG_INF, my = NEG_INF;
 #pragma unroll 1
@@ -599,9 +613,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           const float m_new = fmaxf(m_ref, mx), y_new = fmaxf(y_ref, my);
           l_sum *= m_new == NEG_INF ? 1.f : ex2(m_ref - m_new);
           const float al = y_new == NEG_INF ? 1.f : ex2(y_ref - y_new);
-          if (j > g) {
-            // O may change once P_(j-2) V_(j-2) is in it
-            ok = wait(&sh.pvdone[g], ((j - 2) >> 1) & 1);
+          if (j > 0) {
+            // O may change once P_(j-1) V_(j-1) is in it
+            ok = wait(&sh.pvdone[g], (j - 1) & 1);
             if (!ok) break;
             umma::fence_after();
 #pragma unroll 1
@@ -629,13 +643,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         }
         l_sum += sum;
 #pragma unroll
-        for (int i = 0; i < TOK / 2; i += 16) st16(ts + i, reinterpret_cast<const uint32_t(&)[16]>(pk[i]));
+        for (int i = 0; i < HALF / 2; i += 16) st16(ts + i, reinterpret_cast<const uint32_t(&)[16]>(pk[i]));
         // ---- values that some rows must not see: NaN and infinities there
         // would reach them as 0 * NaN.  They are taken out of the tile and
         // added to O in the rows that see them (a weight is positive) ----
         if (!LIST && (ck >= c1 || (ck + 1) * TOK > min_len)) {
           ok = wait(&sh.vfull[j % NV], (j / NV) & 1);
-          if (ok && j > g) ok = wait(&sh.pvdone[g], ((j - 2) >> 1) & 1);
+          if (ok && j > 0) ok = wait(&sh.pvdone[g], (j - 1) & 1);
           umma::fence_after();
           uint8_t *vt = v_s + (j % NV) * TILE;
           constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u;
@@ -644,8 +658,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             if (!(ok = meet())) break;
             if (r == 0) sh.n_bad[g] = 0;
             if (!(ok = meet())) break;
-            for (int p = 0; p < (r < TOK ? DH / 8 : 0); ++p) {
-              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(r, p, BLK));
+            for (int p = 0; p < (r < HALF ? DH / 8 : 0); ++p) {
+              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(g * HALF + r, p, BLK));
               const uint4 q = *reinterpret_cast<const uint4 *>(e);
               const uint32_t w[4] = {q.x, q.y, q.z, q.w};
               bool any = false;
@@ -681,12 +695,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         }
         st_wait();
         umma::fence_before();
-        mbar_arrive(&sh.pfull[j & 3]);
+        mbar_arrive(&sh.pfull[g][j & 1]);
       }
       // ---- the two sets' O meet where the rings were (every tile of them has
       // been used once both sets' last products are done) ----
-      if (ok && n > 0) ok = wait(&sh.pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1);
-      if (ok && n > 1) ok = wait(&sh.pvdone[n & 1], ((n - 2) >> 1) & 1);
+      if (ok && n > 0) ok = wait(&sh.pvdone[0], (n - 1) & 1) && wait(&sh.pvdone[1], (n - 1) & 1);
       umma::fence_after();
       float *other = reinterpret_cast<float *>(k_s);                 // [DH / 4][M] float4: thread by thread
       float4 *other_ml = reinterpret_cast<float4 *>(k_s + M * DH * 4);  // [M]
@@ -750,7 +763,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_inval(&sh.kfull[i]), mbar_inval(&sh.vfull[i]), mbar_inval(&sh.kempty[i]), mbar_inval(&sh.vempty[i]);
       for (int i = 0; i < 8; ++i)
         for (int v = 0; v < 2; ++v) mbar_inval(&sh.rawfull[v][i]), mbar_inval(&sh.rawempty[v][i]);
-      for (int i = 0; i < 4; ++i) mbar_inval(&sh.sfull[i]), mbar_inval(&sh.pfull[i]);
+      for (int i = 0; i < 2; ++i) mbar_inval(&sh.sfull[i]), mbar_inval(&sh.pfull[0][i]), mbar_inval(&sh.pfull[1][i]);
       for (int i = 0; i < 2; ++i) mbar_inval(&sh.pvdone[i]), mbar_inval(&sh.placed[i]), mbar_inval(&sh.scan[i]);
       mbar_inval(&sh.done), mbar_inval(&sh.joined);
     }
