@@ -26,12 +26,12 @@
 //
 // Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
 // bf16 before they meet the values.  e4m3 caches: codes are exact in f16; a
-// query row is scaled by a power of two into f16's range (bf16 has 8
-// significant bits, so elements down to 2^-24 of the row's largest stay
-// exact); the weights of the sum are e^(s_t - ref) in fp32, and what meets the
-// value codes is e^(s_t - ref) v_scale_t 2^-c in f16, with c such that the
-// row's largest contribution lies in [2^-8, 2^8]: the largest contribution
-// sets f16's range, not the largest scale.
+// tile's queries are scaled by a power of two into f16's range (bf16 has 8
+// significant bits, so elements down to 2^-24 of the tile's largest stay
+// exact).  With ref the running maximum of s_t + ln v_scale_t, the sum of the
+// weights e^(s_t - ref) stays in fp32, and what meets the value codes is
+// e^(s_t - ref) v_scale_t in f16: a row's largest contribution, not its
+// largest scale, sets f16's range.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -95,7 +95,7 @@ struct Cfg {
   static constexpr int OROW = DH + 8;  // floats between rows of a warp's result
   static constexpr size_t RING = (size_t)NW * STAGES * STAGE;
   // results of the warps, and of the CTA
-  static constexpr size_t JOIN = (size_t)NW * R * (OROW * 4 + 16) + (size_t)R * (DH * 4 + 16);
+  static constexpr size_t JOIN = (size_t)NW * R * (OROW * 4 + 8) + (size_t)R * (DH * 4 + 8);
   static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
 };
 
@@ -111,12 +111,10 @@ __device__ __forceinline__ int v_piece(int r, int c) {
   return RB >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
 }
 
-// LIST: blockIdx.x = query * row_tiles + tile of its G heads.  Otherwise
-// blockIdx.x = tile of `per` queries * row_tiles + tile of their rows, with
-// row_tiles > 1 only for per == 1.
+// blockIdx.x: a query (LIST), or a tile of up to `per` queries of a sequence.
 template <class F, bool LIST>
 __global__ void __launch_bounds__(F::THREADS, F::CTAS)
-    attend_kernel(KvView c, AttendView a, Split split, int per, int row_tiles) {
+    attend_kernel(KvView c, AttendView a, Split split, int per) {
   grid_dep_sync();
   constexpr int DH = F::DH, NR = F::NR, R = F::R, RB = F::RB, CPR = F::CPR, KT = F::KT, CH = F::CH,
                 MTL = F::MTL;
@@ -129,16 +127,14 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
   const int G = a.H / c.H_kv, hk = blockIdx.y, Z = split.Z;
-  const int row_tile = blockIdx.x % row_tiles, g0 = row_tile * R;
-  int tile_i = blockIdx.x / row_tiles;
-  const int tile_step = gridDim.x / row_tiles;
+  int tile_i = blockIdx.x;
   Tile t = {tile_i, 1, 0};
   if (!LIST) t = find_tile<F::THREADS>(a, per, tile_i);
 
   for (; t.n > 0;) {
-    const int n_rows = per > 1 ? t.n * G : min(G - g0, R);
-    auto row_query = [&](int r) { return per > 1 ? t.q0 + r / G : t.q0; };
-    auto row_head = [&](int r) { return hk * G + (per > 1 ? r % G : g0 + r); };
+    const int n_rows = t.n * G;  // at most R
+    auto row_query = [&](int r) { return LIST ? t.q0 : t.q0 + r / G; };
+    auto row_head = [&](int r) { return hk * G + (LIST ? r : r % G); };
 
     // ---- the tile's tokens: prefix (or list) chunks, then drafted chunks ----
     int seq = -1, len = 0, cb, ce;
@@ -195,42 +191,41 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     // ---- query fragments, the k dimension permuted so that a lane's 16-byte
     // pieces of a key row feed whole A fragments ----
     uint2 qf[Q_SMEM ? 1 : KT][Q_SMEM ? 1 : NR];
-    float mul[NR][2];  // scale log2(e), over the row's power of two
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      if (Q_SMEM && n % NW != warp % NR) continue;  // warps beyond NR repeat, harmlessly
+    float sc = 1.f;
+    auto row_piece = [&](int n, int i) {
       const int r = n * 8 + g;
-      const bool live = r < n_rows;
-      const uint16_t *src = a.q + ((int64_t)row_query(live ? r : 0) * a.H + row_head(live ? r : 0)) * DH;
-      uint4 raw[DH / 32];
+      // e4m3: 16 elements at 64 ch + 16 c4 (pieces 2 ch, 2 ch + 1 of the lane);
+      // bf16: 8 at 32 i + 8 c4
+      const int d0 = FP8 ? 64 * (i >> 1) + 16 * c4 + 8 * (i & 1) : 32 * i + 8 * c4;
+      return r < n_rows ? *reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH + d0)
+                        : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (FP8) {
+      float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        // FP8: 16 elements at 64 ch + 16 c4 (pieces 2 ch, 2 ch + 1 of the
-        // lane); bf16: 8 at 32 i + 8 c4
-        const int d0 = FP8 ? 64 * (i >> 1) + 16 * c4 + 8 * (i & 1) : 32 * i + 8 * c4;
-        raw[i] = live ? *reinterpret_cast<const uint4 *>(src + d0) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      float sc = 1.f;
-      if (FP8) {
-        float m = 0.f;
-        auto take = [&](float x) { m = (x > m || x != x) ? x : m; };  // a NaN stays
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
-          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint4 v = row_piece(n, i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const float2 f = bf16x2_to_float2(w[p]);
-            take(fabsf(f.x));
-            take(fabsf(f.y));
+            m = finite_max(finite_max(m, f.x), f.y);
           }
         }
-        take(__shfl_xor_sync(0xffffffffu, m, 1));
-        take(__shfl_xor_sync(0xffffffffu, m, 2));
-        sc = row_scale(m);
-      }
+#pragma unroll
+      for (int b = 1; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+      sc = f16_scale(m);
+    }
+    const float mul = a.scale * LOG2E / sc;  // of a product, to a base-2 logit
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      if (Q_SMEM && n != warp % NR) continue;  // a warp's share (warps beyond NR repeat, harmlessly)
 #pragma unroll
       for (int i = 0; i < DH / 32; ++i) {
-        uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const uint4 v = row_piece(n, i);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (FP8) {
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -240,46 +235,26 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint2 v = make_uint2(w[2 * u], w[2 * u + 1]);
+          const uint2 x = make_uint2(w[2 * u], w[2 * u + 1]);
           if (Q_SMEM)
-            q_s[(((2 * i + u) * (NR / 2) + n / 2) * 32 + lane) * 2 + (n & 1)] = v;
+            q_s[(((2 * i + u) * (NR / 2) + n / 2) * 32 + lane) * 2 + (n & 1)] = x;
           else
-            qf[2 * i + u][n] = v;
+            qf[2 * i + u][n] = x;
         }
       }
-      // the multiplier of the lane's columns sits with the lanes of those rows
-      if (!Q_SMEM) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          mul[n][x] = a.scale * LOG2E / __shfl_sync(0xffffffffu, sc, (2 * c4 + x) * 4);
-      } else if (c4 == 0) {
-        reinterpret_cast<float *>(smem)[r] = sc;  // read before the rings are filled
-      }
     }
-    if (Q_SMEM) {
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) mul[n][x] = a.scale * LOG2E / reinterpret_cast<float *>(smem)[n * 8 + 2 * c4 + x];
-      __syncthreads();
-    }
+    if (Q_SMEM) __syncthreads();
 
     float o[KT][NR][4];
-    // base 2, per column: reference of the weights' sum and the sum (this
-    // lane's tokens), reference of O (bf16 caches: the same) and the factor
-    // between the two
-    float m_ref[NR][2], l_sum[NR][2], y_ref[NR][2], fac[NR][2];
+    // per column: base-2 reference of O and of the weights' sum, and the sum
+    // over this lane's tokens
+    float y_ref[NR][2], l_sum[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
       for (int j = 0; j < KT; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        m_ref[n][x] = y_ref[n][x] = NEG_INF;
-        l_sum[n][x] = 0.f;
-        fac[n][x] = 1.f;
-      }
+      y_ref[n][0] = y_ref[n][1] = NOTHING;
+      l_sum[n][0] = l_sum[n][1] = 0.f;
     }
 
     uint8_t *ring = smem + warp * (STAGES * F::STAGE);
@@ -449,10 +424,11 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 
       // ---- weights of the tokens g + 8 y for the columns x: p = e^(s - ref)
       // for the sum, w for the values ----
-      float ks[2 * MTL], vs[2 * MTL];
-      if (FP8) {
+      float km[2 * MTL], vs[2 * MTL];
 #pragma unroll
-        for (int y = 0; y < 2 * MTL; ++y) ks[y] = ss[g + 8 * y], vs[y] = ss[CH + g + 8 * y];
+      for (int y = 0; y < 2 * MTL; ++y) {
+        km[y] = FP8 ? ss[g + 8 * y] * mul : mul;
+        vs[y] = FP8 ? ss[CH + g + 8 * y] : 1.f;
       }
       float p[NR][4 * MTL], w[NR][4 * MTL];
       auto logit = [&](auto m, float v, int n, int x, int y) {
@@ -467,48 +443,36 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
             for (int y = 0; y < 2 * MTL; ++y) {
               const int e = 2 * y + x;
-              const float v = logit(m, fmaf(s[n][y >> 1][e & 3], FP8 ? ks[y] * mul[n][x] : mul[n][x], -m_ref[n][x]), n, x, y);
+              const float v = logit(m, fmaf(s[n][y >> 1][e & 3], km[y], -y_ref[n][x]), n, x, y);
               p[n][e] = ex2(v);
-              w[n][e] = p[n][e];
-              if (FP8) {
-                w[n][e] *= vs[y] * fac[n][x];
-                // (rows gathered for others may hold any scale)
-                if (!LIST && m.value && v == NEG_INF) w[n][e] = 0.f;
-              }
-              top = fmaxf(top, fmaxf(p[n][e], w[n][e]));
+              w[n][e] = FP8 ? p[n][e] * vs[y] : p[n][e];
+              // (rows gathered for others may hold any scale)
+              if (FP8 && !LIST && m.value && v == NEG_INF) w[n][e] = 0.f;
+              top = fmaxf(top, w[n][e]);
             }
         return __any_sync(0xffffffffu, top > LAZY);
       };
       for (bool again = false;; again = true) {
         const bool above = masked ? weigh(std::true_type()) : weigh(std::false_type());
-        // the first chunk comes here with ref = -inf, p = inf
+        // (the first visible token always comes out above)
         if (again || !above) break;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = NEG_INF, my = NEG_INF;
+            float my = NEG_INF;
 #pragma unroll
-            for (int y = 0; y < 2 * MTL; ++y) {
-              const float v = logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * (FP8 ? ks[y] * mul[n][x] : mul[n][x]), n, x, y);
-              mx = fmaxf(mx, v);
-              if (FP8) my = fmaxf(my, v + __log2f(vs[y] < 0x1p-100f ? 0x1p-100f : vs[y]));  // a NaN stays
-            }
+            for (int y = 0; y < 2 * MTL; ++y)
+              my = fmaxf(my, logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * km[y], n, x, y) +
+                                 (FP8 ? log2_scale(vs[y]) : 0.f));
 #pragma unroll
-            for (int b = 4; b < 32; b <<= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, b));
-              if (FP8) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));
-            }
-            if (!FP8) my = mx;
-            const float m_new = fmaxf(m_ref[n][x], mx), y_new = fmaxf(y_ref[n][x], my);
-            // a column without a visible token yet keeps -inf: its sums are 0
-            l_sum[n][x] *= m_new == NEG_INF ? 1.f : ex2(m_ref[n][x] - m_new);
-            const float al = y_new == NEG_INF ? 1.f : ex2(y_ref[n][x] - y_new);
+            for (int b = 4; b < 32; b <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));
+            const float y_new = fmaxf(y_ref[n][x], my);
+            const float al = ex2(y_ref[n][x] - y_new);
+            l_sum[n][x] *= al;
 #pragma unroll
             for (int j = 0; j < KT; ++j) o[j][n][x] *= al, o[j][n][2 + x] *= al;
-            m_ref[n][x] = m_new;
             y_ref[n][x] = y_new;
-            fac[n][x] = m_new == NEG_INF || !FP8 ? 1.f : ex2(m_new - y_new);
           }
       }
       uint32_t pb[NR][2 * MTL];
@@ -604,7 +568,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 
     // ---- join the warps ----
     float *so = reinterpret_cast<float *>(smem);                                      // [NW][R][OROW]
-    float4 *sml = reinterpret_cast<float4 *>(smem + (size_t)NW * R * F::OROW * 4);  // [NW][R]
+    float2 *syl = reinterpret_cast<float2 *>(smem + (size_t)NW * R * F::OROW * 4);  // [NW][R]
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -613,7 +577,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
         for (int b = 4; b < 32; b <<= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
         const int r = warp * R + n * 8 + 2 * c4 + x;
-        if (g == 0) sml[r] = make_float4(m_ref[n][x], l, y_ref[n][x], 0.f);
+        if (g == 0) syl[r] = make_float2(y_ref[n][x], l);
         float *row = so + (size_t)r * F::OROW;
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
@@ -626,21 +590,21 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         }
       }
     __syncthreads();
-    float *jo = reinterpret_cast<float *>(sml + NW * R);  // [R][DH]: this CTA's share
-    float4 *jml = reinterpret_cast<float4 *>(jo + R * DH);  // [R]
+    float *jo = reinterpret_cast<float *>(syl + NW * R);    // [R][DH]: this CTA's share
+    float2 *jyl = reinterpret_cast<float2 *>(jo + R * DH);  // [R]
     const bool in_cluster = Z > 1 && split.o == nullptr;
     auto out_row = [&](int r) { return (int64_t)row_query(r) * a.H + row_head(r); };
     for (int e = tid; e < n_rows * (DH / 4); e += F::THREADS) {
       const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
       const Part p = join_parts<NW>(
-          NW, [&](int w) { return sml[w * R + r]; },
+          NW, [&](int w) { return syl[w * R + r]; },
           [&](int w) { return *reinterpret_cast<const float4 *>(so + ((size_t)w * R + r) * F::OROW + d0); });
       if (Z == 1) {
         store_row(a, p, out_row(r), DH, d0);
       } else {
         const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + out_row(r);
         *reinterpret_cast<float4 *>(in_cluster ? jo + r * DH + d0 : split.o + prow * DH + d0) = p.v;
-        if (d0 == 0) *(in_cluster ? jml + r : split.ml + prow) = make_float4(p.M, p.l, p.Y, 0.f);
+        if (d0 == 0) *(in_cluster ? jyl + r : split.yl + prow) = make_float2(p.Y, p.l);
       }
     }
     if (in_cluster) {
@@ -649,12 +613,12 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       for (int e = blockIdx.z * F::THREADS + tid; e < n_rows * (DH / 4); e += Z * F::THREADS) {
         const int r = e / (DH / 4), d0 = (e % (DH / 4)) * 4;
         const Part p = join_parts<8>(
-            Z, [&](int z) { return ld_cluster(jml + r, z); }, [&](int z) { return ld_cluster(jo + r * DH + d0, z); });
+            Z, [&](int z) { return ld_cluster2(jyl + r, z); }, [&](int z) { return ld_cluster4(jo + r * DH + d0, z); });
         store_row(a, p, out_row(r), DH, d0);
       }
       cluster_sync();  // no CTA overwrites or leaves what another still reads
     }
-    tile_i += tile_step;
+    tile_i += gridDim.x;
     if (LIST || tile_i >= t.total) break;
     __syncthreads();
     t = find_tile<F::THREADS>(a, per, tile_i);
@@ -666,44 +630,50 @@ template <int DH>
 __global__ void __launch_bounds__(DH) attend_combine_kernel(AttendView a, Split split) {
   grid_dep_sync();
   constexpr int LANES = DH / 4;
-  __shared__ float4 ml_s[4], v_s[4][LANES];
+  __shared__ float2 yl_s[4];
+  __shared__ float4 v_s[4][LANES];
   const int64_t row = blockIdx.x, n = (int64_t)a.n_q * a.H;
   const int part = threadIdx.x / LANES, lane = threadIdx.x % LANES;
   const Part p = join_parts<4>(
-      (split.Z - part + 3) / 4, [&](int i) { return split.ml[(int64_t)(4 * i + part) * n + row]; },
+      (split.Z - part + 3) / 4, [&](int i) { return split.yl[(int64_t)(4 * i + part) * n + row]; },
       [&](int i) {
         return *reinterpret_cast<const float4 *>(split.o + ((int64_t)(4 * i + part) * n + row) * DH + 4 * lane);
       });
   v_s[part][lane] = p.v;
-  if (lane == 0) ml_s[part] = make_float4(p.M, p.l, p.Y, 0.f);
+  if (lane == 0) yl_s[part] = make_float2(p.Y, p.l);
   __syncthreads();
   if (part) return;
-  store_row(a, join_parts<4>(4, [&](int i) { return ml_s[i]; }, [&](int i) { return v_s[i][lane]; }), row, DH, 4 * lane);
+  store_row(a, join_parts<4>(4, [&](int i) { return yl_s[i]; }, [&](int i) { return v_s[i][lane]; }), row, DH, 4 * lane);
 }
 
 struct Plan {
-  int nr;         // n-tiles of 8 rows per CTA
-  int per;        // queries per tile (1 with lists)
-  int row_tiles;  // tiles of a query's G rows (per == 1)
+  int nr;        // n-tiles of 8 rows per CTA
+  int per;       // queries per tile (1 with lists)
   int tiles, Z;
-  bool cluster;   // the Z shares are a cluster
-  bool umma;      // tiles of up to 128 rows on tcgen05 (attend_umma.cu)
+  bool cluster;  // the Z shares are a cluster
+  bool umma;     // tiles of up to 128 rows on tcgen05 (attend_umma.cu)
 };
 
-// Rows of a tile: as many n-tiles as one query's G heads (and, without lists,
-// its sequence's neighbours) fill, 32 rows at the most.  Lengths are on the
-// device: whole prefixes count as full caches, and the batch's queries as
-// spread evenly over the sequences (a CTA goes on to the tiles beyond the
-// grid where they are not).
+// Rows of a tile: one query's G heads and, without lists, those of its
+// sequence's neighbours.  Lengths are on the device: whole prefixes count as
+// full caches, and the batch's queries as spread evenly over the sequences (a
+// CTA goes on to the tiles beyond the grid where they are not).
+//
+// More than 16 rows without lists, or 32 with them, go to the tcgen05 kernel.
+// Measured on both (us, mma.sync / tcgen05; 8 sequences, 8 key/value heads of
+// 128): 12 rows over 16K bf16 tokens 89 / 98 and e4m3 74 / 170, 24 rows 152 /
+// 100 and 249 / 172; 12 rows over 1000 tokens 21 / 25 and 21 / 35, 24 rows
+// 29 / 27 and 33 / 36; lists of 2048 tokens (2 key/value heads), 16 rows 12 /
+// 16 and 12 / 21, 32 rows 16 / 16 and 18 / 21.
 Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   Plan p;
   const int G = H / c.H_kv;
   const bool list = k > 0;
   const int seqs = std::max(1, std::min(n_q, c.n_seq)), per_seq = cdiv(std::max(n_q, 1), seqs);
   const int rows = list ? G : G * std::min(per_seq, 128);
-  p.umma = rows > 32;
+  p.umma = rows > (list ? 32 : 16);
   if (p.umma) {
-    p.nr = 0, p.row_tiles = 1, p.cluster = false;
+    p.nr = 0, p.cluster = false;
     p.per = list ? 1 : 128 / G;
     p.tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
     const int chunks = cdiv(list ? k : c.L_cap, 128) + cdiv(n_draft, 128);
@@ -722,11 +692,10 @@ Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   p.nr = rows > 16 ? 4 : rows > 8 ? 2 : 1;
   const int R = 8 * p.nr;
   p.per = list ? 1 : std::max(1, R / G);
-  p.row_tiles = p.per > 1 ? 1 : cdiv(G, R);
   p.tiles = list ? n_q : seqs * cdiv(per_seq, p.per);
   const int ch = chunk_tokens(c.fp8, p.nr), chunks = cdiv(list ? k : c.L_cap, ch) + cdiv(n_draft, ch);
   const int ctas = ctas_per_sm(c.fp8, c.d, p.nr);
-  const int64_t units = (int64_t)p.tiles * p.row_tiles * c.H_kv;
+  const int64_t units = (int64_t)p.tiles * c.H_kv;
   // shares: fill the SMs once, two chunks per warp at the least.  A cluster of
   // up to 8 joins them without a second launch; more shares pay off only
   // where each of 8 would still run through 32 chunks per warp or more.
@@ -742,17 +711,18 @@ cudaError_t run_attend(const KvView &c, const AttendView &a, const Split &sp, co
   struct Tag {};
   const int have = cached_per_device<Tag>([] { return opt_in_max_dyn_smem(attend_kernel<F, LIST>); });
   if (have < (int)F::SMEM) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(p.tiles * p.row_tiles), c.H_kv, p.Z), block(F::THREADS);
+  const dim3 grid((unsigned)p.tiles, c.H_kv, p.Z), block(F::THREADS);
   return p.cluster ? launch_kernel_cluster(attend_kernel<F, LIST>, grid, block, dim3(1, 1, p.Z), F::SMEM, s, c, a, sp,
-                                           p.per, p.row_tiles)
-                   : launch_kernel(attend_kernel<F, LIST>, grid, block, F::SMEM, s, c, a, sp, p.per, p.row_tiles);
+                                           p.per)
+                   : launch_kernel(attend_kernel<F, LIST>, grid, block, F::SMEM, s, c, a, sp, p.per);
 }
 
 template <int DH, bool FP8, bool LIST>
 cudaError_t pick_rows(const KvView &c, const AttendView &a, const Split &sp, const Plan &p, cudaStream_t s) {
-  return p.nr == 1   ? run_attend<Cfg<DH, FP8, 1>, LIST>(c, a, sp, p, s)
-         : p.nr == 2 ? run_attend<Cfg<DH, FP8, 2>, LIST>(c, a, sp, p, s)
-                     : run_attend<Cfg<DH, FP8, 4>, LIST>(c, a, sp, p, s);
+  if (p.nr == 1) return run_attend<Cfg<DH, FP8, 1>, LIST>(c, a, sp, p, s);
+  if constexpr (LIST)
+    if (p.nr == 4) return run_attend<Cfg<DH, FP8, 4>, LIST>(c, a, sp, p, s);
+  return run_attend<Cfg<DH, FP8, 2>, LIST>(c, a, sp, p, s);
 }
 
 template <int DH, bool FP8>
@@ -768,7 +738,7 @@ size_t attend_ws_bytes(const KvView &c, int n_q, int H, int k, int n_draft) {
   const Plan p = make_plan(c, n_q, H, k, n_draft);
   if (p.Z <= 1 || p.cluster) return 0;
   const size_t n = (size_t)p.Z * n_q * H;
-  return round256(n * c.d * 4) + round256(n * 16);
+  return round256(n * c.d * 4) + round256(n * 8);
 }
 
 cudaError_t launch_attend(const KvView &c, const AttendView &a, void *ws, cudaStream_t s) {
@@ -777,7 +747,7 @@ cudaError_t launch_attend(const KvView &c, const AttendView &a, void *ws, cudaSt
   Split sp = {nullptr, nullptr, p.Z};
   if (p.Z > 1 && !p.cluster) {
     sp.o = static_cast<float *>(ws);
-    sp.ml = reinterpret_cast<float4 *>(static_cast<uint8_t *>(ws) + round256((size_t)p.Z * a.n_q * a.H * c.d * 4));
+    sp.yl = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + round256((size_t)p.Z * a.n_q * a.H * c.d * 4));
   }
   cudaError_t e = p.umma       ? launch_attend_umma(c, a, sp, p.per, p.tiles, s)
                   : c.d == 128 ? (c.fp8 ? pick_attend<128, true>(c, a, sp, p, s) : pick_attend<128, false>(c, a, sp, p, s))

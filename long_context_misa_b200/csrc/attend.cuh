@@ -10,6 +10,9 @@ constexpr float LAZY = 256.f;  // most that a weight may reach before its refere
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NEG_INF = -__builtin_huge_valf();
+// reference of a row that has seen nothing: finite, so that a logit of -inf
+// still weighs 0 against it, and far enough down that any other logit moves it
+constexpr float NOTHING = -3e38f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -34,13 +37,24 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 2^(7 - E) for amax = m 2^E, m in [0.5, 1): the row's largest element lands
-// in [64, 128).  1 for rows of zeros or with a NaN or infinity.
-__device__ __forceinline__ float row_scale(float amax) {
-  if (!(amax > 0.f) || !isfinite(amax)) return 1.f;
+// 2^(7 - E) for amax = m 2^E, m in [0.5, 1): the largest element lands in
+// [64, 128).  1 for zeros.
+__device__ __forceinline__ float f16_scale(float amax) {
+  if (!(amax > 0.f)) return 1.f;
   const int e = 7 - ((int)(__float_as_uint(amax) >> 23) - 126);
   return ldexpf(1.f, min(max(e, -126), 126));
 }
+
+// max(m, |x|), where x is finite
+__device__ __forceinline__ float finite_max(float m, float x) {
+  const float y = fabsf(x);
+  return y < __int_as_float(0x7f800000) ? fmaxf(m, y) : m;
+}
+
+// log2 of a value scale for the reference of O, held within [-100, 100]: a row
+// of zeros (scale 0) or one that held an infinity must not move the others'
+// reference out of fp32's range.
+__device__ __forceinline__ float log2_scale(float s) { return __log2f(fminf(fmaxf(s, 0x1p-100f), 0x1p100f)); }
 
 // Prefix length of query i (0 for none) and its sequence (-1: outside the
 // cache, it sees nothing).
@@ -147,33 +161,28 @@ __device__ Tile find_tile(const AttendView &a, int per, int want) {
 
 struct Split {
   float *o;    // [Z][n_q * H][DH]; nullptr: the Z shares are a cluster
-  float4 *ml;  // [Z][n_q * H] (max, sum, reference of O)
+  float2 *yl;  // [Z][n_q * H] (reference, sum)
   int Z;
 };
 
-// One row's joined parts: base-2 maximum of the logits, sum of the weights
-// relative to it, reference of v.
+// A part of a row: O and the sum of weights, both relative to 2^Y.
 struct Part {
-  float M = NEG_INF, Y = NEG_INF, l = 0.f;
+  float Y = NOTHING, l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
-// Join n parts: ml(i) = (max, sum, reference), v(i) = 4 elements of O.
-template <int UNROLL, class ML, class V>
-__device__ __forceinline__ Part join_parts(int n, ML &&ml, V &&v) {
+// Join n parts: yl(i) = (reference, sum), v(i) = 4 elements of O.
+template <int UNROLL, class YL, class V>
+__device__ __forceinline__ Part join_parts(int n, YL &&yl, V &&v) {
   Part p;
 #pragma unroll UNROLL
-  for (int i = 0; i < n; ++i) {
-    const float4 m = ml(i);
-    p.M = fmaxf(p.M, m.x);
-    p.Y = fmaxf(p.Y, m.z);
-  }
-  const float ref = p.M == NEG_INF ? 0.f : p.M, yref = p.Y == NEG_INF ? 0.f : p.Y;
+  for (int i = 0; i < n; ++i) p.Y = fmaxf(p.Y, yl(i).x);
 #pragma unroll UNROLL
   for (int i = 0; i < n; ++i) {
-    const float4 m = ml(i), x = v(i);
-    const float f = ex2(m.z - yref);
-    p.l = fmaf(m.y, ex2(m.x - ref), p.l);
+    const float2 a = yl(i);
+    const float4 x = v(i);
+    const float f = ex2(a.x - p.Y);
+    p.l = fmaf(a.y, f, p.l);
     p.v.x = fmaf(x.x, f, p.v.x), p.v.y = fmaf(x.y, f, p.v.y), p.v.z = fmaf(x.z, f, p.v.z), p.v.w = fmaf(x.w, f, p.v.w);
   }
   return p;
@@ -181,11 +190,11 @@ __device__ __forceinline__ Part join_parts(int n, ML &&ml, V &&v) {
 
 // 4 elements of a finished row, and (d0 == 0) its lse.
 __device__ __forceinline__ void store_row(const AttendView &a, const Part &p, int64_t row, int DH, int d0) {
-  const bool none = p.M == NEG_INF && p.l == 0.f;
-  const float inv = none ? 0.f : ex2((p.Y == NEG_INF ? 0.f : p.Y) - (p.M == NEG_INF ? 0.f : p.M)) / p.l;
+  const bool none = p.l == 0.f;  // (a NaN is not)
+  const float inv = none ? 0.f : 1.f / p.l;
   *reinterpret_cast<uint2 *>(a.out + row * DH + d0) =
       make_uint2(bf16x2(p.v.x * inv, p.v.y * inv), bf16x2(p.v.z * inv, p.v.w * inv));
-  if (a.lse && d0 == 0) a.lse[row] = none ? NEG_INF : p.M * LN2 + logf(p.l);
+  if (a.lse && d0 == 0) a.lse[row] = none ? NEG_INF : (p.Y + log2f(p.l)) * LN2;
 }
 
 // every thread of every CTA of the cluster; shared-memory writes before it are
@@ -193,15 +202,23 @@ __device__ __forceinline__ void store_row(const AttendView &a, const Part &p, in
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's p
-__device__ __forceinline__ float4 ld_cluster(const void *p, uint32_t rank) {
+// the shared memory of CTA `rank` of the cluster, at this CTA's p
+__device__ __forceinline__ uint32_t cluster_at(const void *p, uint32_t rank) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float4 ld_cluster4(const void *p, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
+               : "r"(cluster_at(p, rank))
                : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(const void *p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_at(p, rank)) : "memory");
   return v;
 }
 

@@ -54,7 +54,7 @@ struct UCfg {
   static constexpr int NK = FP8 ? (DH > 64 ? 1 : 2) : DH > 64 ? 2 : 4, NV = FP8 ? (DH > 64 ? 2 : 3) : DH > 64 ? 3 : 5;
   static constexpr int NR = FP8 ? (DH > 64 ? 2 : 4) : 0;
   static constexpr int SMEM = QTILE + (NK + NV) * TILE + 2 * NR * RAW + 1024;
-  static_assert((NK + NV) * TILE >= M * (DH * 4 + 16), "the odd set's result takes the rings' place");
+  static_assert((NK + NV) * TILE >= M * (DH * 4 + 8), "a set's result takes the rings' place");
   static_assert(2 * GROUP == TOK && NV + NR + 2 <= SLOTS, "masks and scales outlive their chunk");
 };
 constexpr int MAX_STAGES = 5;
@@ -69,8 +69,7 @@ struct Shared {
   int row_idx[2][2][TOK];   // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
   uint32_t have[SLOTS][2 * W];  // which tokens of a chunk are there
   int len[M], query[M];
-  float mul[M];  // scale log2(e), over the row's power of two (e4m3 caches)
-  int seq, max_len, min_len;
+  int seq, max_len, min_len, q_max;
   int n_bad[2];
   int2 bad_at[2][BAD];  // (token, element)
   float bad_val[2][BAD];
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_init(&sh.pvdone[i], 1), mbar_init(&sh.placed[i], GROUP), mbar_init(&sh.scan[i], 128);
       mbar_init(&sh.done, 1), mbar_init(&sh.joined, 256);
       fence_mbar_init();
-      sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff;
+      sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff, sh.q_max = 0;
     }
     __syncthreads();
     if (tid < M) {
@@ -209,27 +208,34 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       sh.query[r] = r < n_rows ? row_query(r) : -1;
     }
     // ---- Q: 16-bit rows, K-major with 128-byte swizzle; e4m3 caches: f16
-    // after a power of two per row.  DH / 8 lanes hold a row ----
-    constexpr int QL = DH / 8, QT = THREADS - M;  // (the other threads look up the rows meanwhile)
-    for (int e = tid - M; tid >= M && e < (M * QL + QT - 1) / QT * QT; e += QT) {
-      const int r = min(e / QL, M - 1), p = e % QL;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (e < M * QL && r < n_rows)
-        v = reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH)[p];
-      if (FP8) {
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float m = 0.f;
-        auto take = [&](float x) { m = (x > m || x != x) ? x : m; };  // a NaN stays
+    // after a power of two ----
+    constexpr int QL = DH / 8, QT = THREADS - M;  // pieces of a row; threads (the others look up the rows meanwhile)
+    auto q_piece = [&](int r, int p) {
+      return r < n_rows ? reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH)[p]
+                        : make_uint4(0u, 0u, 0u, 0u);
+    };
+    float sc = 1.f;
+    if (FP8) {
+      float m = 0.f;
+      for (int e = tid - M; tid >= M && e < n_rows * QL; e += QT) {
+        const uint4 v = q_piece(e / QL, e % QL);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = bf16x2_to_float2(w[i]);
-          take(fabsf(f.x));
-          take(fabsf(f.y));
+          m = finite_max(finite_max(m, f.x), f.y);
         }
-#pragma unroll
-        for (int o = 1; o < QL; o <<= 1) take(__shfl_xor_sync(0xffffffffu, m, o));
-        const float sc = row_scale(m);
-        if (p == 0 && e < M * QL) sh.mul[r] = a.scale * LOG2E / sc;
+      }
+      atomicMax(&sh.q_max, __float_as_int(m));  // (positive floats order as integers)
+      __syncthreads();
+      sc = f16_scale(__int_as_float(sh.q_max));
+    }
+    const float mul = a.scale * LOG2E / sc;  // of a product, to a base-2 logit
+    for (int e = tid - M; tid >= M && e < M * QL; e += QT) {
+      const int r = e / QL, p = e % QL;
+      uint4 v = q_piece(r, p);
+      if (FP8) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = bf16x2_to_float2(w[i]);
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         }
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (e < M * QL) *reinterpret_cast<uint4 *>(q_s + tile_at(r, p, F::QBLK)) = v;
+      *reinterpret_cast<uint4 *>(q_s + tile_at(r, p, F::QBLK)) = v;
     }
     umma::fence_proxy_async();
     umma::fence_before();
@@ -495,8 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       const int g = warp >> 2, r = tid & 127;
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = tl + T_O + g * 128;
       const int my_len = sh.len[r], my_query = sh.query[r];
-      const float row_mul = FP8 ? sh.mul[r] : a.scale * LOG2E;
-      float m_ref = NEG_INF, y_ref = NEG_INF, fac = 1.f, l_sum = 0.f;
+      float y_ref = NOTHING, l_sum = 0.f;  // base-2 reference of O and of the sum, and the sum
       bool ok = true;
       int scans = 0;
       // bounded waits of a whole warp (its tensor-memory accesses need all lanes)
@@ -572,14 +577,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               }
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                float x = fmaf(__uint_as_float(v[w][i + u]), FP8 ? k4[u] * row_mul : row_mul, -m_ref);
+                float x = fmaf(__uint_as_float(v[w][i + u]), FP8 ? k4[u] * mul : mul, -y_ref);
                 const bool seen = !mk.value || ((see[w] >> (i + u)) & 1u);
                 if (mk.value && !seen) x = NEG_INF;
                 const float p = ex2(x);
                 s4[u] += p;
                 wt[u] = p;
-                if (FP8) wt[u] = seen ? p * (v4[u] * fac) : 0.f;
-                top = FP8 ? fmaxf(top, fmaxf(p, wt[u])) : fmaxf(top, p);
+                if (FP8) wt[u] = seen ? p * v4[u] : 0.f;
+                top = fmaxf(top, wt[u]);
               }
 #pragma unroll
               for (int u = 0; u < 4; u += 2)
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         float sum = 0.f, top = LAZY + 1.f;
         if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
         if (__any_sync(0xffffffffu, top > LAZY)) {
-          float mx = NEG_INF, my = NEG_INF;
+          float my = NEG_INF;
 #pragma unroll 1
           for (int w = 0; w < W; ++w) {
             uint32_t v[32];
@@ -601,18 +606,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             const uint32_t sw = w == 0 ? see[0] : see[1];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = (sw >> i) & 1u ? __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] * row_mul : row_mul) : NEG_INF;
-              mx = fmaxf(mx, x);
-              if (FP8) {
-                const float s = vs[w * 32 + i];
-                my = fmaxf(my, x + __log2f(s < 0x1p-100f ? 0x1p-100f : s));  // a NaN stays
-              }
+              const float x = __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] * mul : mul);
+              if ((sw >> i) & 1u) my = fmaxf(my, FP8 ? x + log2_scale(vs[w * 32 + i]) : x);
             }
           }
-          if (!FP8) my = mx;
-          const float m_new = fmaxf(m_ref, mx), y_new = fmaxf(y_ref, my);
-          l_sum *= m_new == NEG_INF ? 1.f : ex2(m_ref - m_new);
-          const float al = y_new == NEG_INF ? 1.f : ex2(y_ref - y_new);
+          const float y_new = fmaxf(y_ref, my), al = ex2(y_ref - y_new);
+          l_sum *= al;
           if (j > 0) {
             // O may change once P_(j-1) V_(j-1) is in it
             ok = wait(&sh.pvdone[g], (j - 1) & 1);
@@ -635,11 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             st_wait();
           }
           y_ref = y_new;
-          fac = m_new == NEG_INF || !FP8 ? 1.f : ex2(m_new - y_new);
-          // a row that still sees nothing: its masked logits must not meet -inf
-          m_ref = m_new == NEG_INF ? 0.f : m_new;
           masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
-          m_ref = m_new;
         }
         l_sum += sum;
 #pragma unroll
@@ -702,10 +697,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       if (ok && n > 0) ok = wait(&sh.pvdone[0], (n - 1) & 1) && wait(&sh.pvdone[1], (n - 1) & 1);
       umma::fence_after();
       float *other = reinterpret_cast<float *>(k_s);                 // [DH / 4][M] float4: thread by thread
-      float4 *other_ml = reinterpret_cast<float4 *>(k_s + M * DH * 4);  // [M]
+      float2 *other_yl = reinterpret_cast<float2 *>(k_s + M * DH * 4);  // [M]
       const bool live = ok && r < n_rows;
       if (g == 1 && ok) {
-        other_ml[r] = make_float4(m_ref, l_sum, y_ref, 0.f);
+        other_yl[r] = make_float2(y_ref, l_sum);
 #pragma unroll 1
         for (int i = 0; i < DH; i += 32) {
           uint32_t v[32];
@@ -720,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       if (g == 0 && ok && (ok = wait(&sh.joined, 0))) {
         const int64_t orow = live ? (int64_t)row_query(r) * a.H + row_head(r) : 0;
         const int64_t prow = (int64_t)blockIdx.z * a.n_q * a.H + orow;
-        const float4 mine = make_float4(m_ref, l_sum, y_ref, 0.f), theirs = other_ml[r];
+        const float2 mine = make_float2(y_ref, l_sum), theirs = other_yl[r];
         Part ends;
 #pragma unroll 1
         for (int i = 0; i < DH; i += 32) {
@@ -741,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           }
           __syncwarp();
         }
-        if (live && Z > 1) split.ml[prow] = make_float4(ends.M, ends.l, ends.Y, 0.f);
+        if (live && Z > 1) split.yl[prow] = make_float2(ends.Y, ends.l);
       }
       umma::fence_before();
     }
