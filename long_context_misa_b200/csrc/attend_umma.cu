@@ -693,8 +693,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_arrive(&sh.pfull[g][j & 1]);
       }
       // ---- the two sets' O meet where the rings were (every tile of them has
-      // been used once both sets' last products are done) ----
-      if (ok && n > 0) ok = wait(&sh.pvdone[0], (n - 1) & 1) && wait(&sh.pvdone[1], (n - 1) & 1);
+      // been used once all products are done) ----
+      // (pvdone would not do: a set may be two of its phases behind here, and a
+      // parity tells only neighbours apart)
+      if (ok && n > 0) ok = wait(&sh.done, 0);
       umma::fence_after();
       float *other = reinterpret_cast<float *>(k_s);                 // [DH / 4][M] float4: thread by thread
       float2 *other_yl = reinterpret_cast<float2 *>(k_s + M * DH * 4);  // [M]

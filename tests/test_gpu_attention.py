@@ -504,9 +504,10 @@ def test_drafts_outside_the_cache():
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
-def test_interleaved_sequences(e4m3):
+@pytest.mark.parametrize("G", [2, 12])
+def test_interleaved_sequences(e4m3, G):
     """Queries of one sequence not side by side: still right."""
-    c = Case(e4m3, 128, 2, 2, lens=(100, 64, 33), per=(4, 4, 4), seed=37)
+    c = Case(e4m3, 128, 2, G, lens=(100, 64, 33), per=(4, 4, 4), seed=37)
     order = [0, 4, 8, 1, 5, 9, 2, 6, 10, 3, 7, 11]
     c.seq, c.pos = [c.seq[i] for i in order], [c.pos[i] - (i % 3) for i in order]
     c.poison()
@@ -514,10 +515,11 @@ def test_interleaved_sequences(e4m3):
 
 
 @pytest.mark.parametrize("k", [0, 40])
+@pytest.mark.parametrize("G", [1, 3, 12, 40])
 @pytest.mark.parametrize("e4m3", [True, False])
-def test_values_seen_by_some(e4m3, k):
+def test_values_seen_by_some(e4m3, G, k):
     """NaN and infinities in a drafted value or at a causal border reach the queries that see them, no others."""
-    c = Case(e4m3, 128, 2, 3, lens=(70, 90), per=(6, 6), k=k, drafts=6, seed=38)
+    c = Case(e4m3, 128, 2, G, lens=(70, 90), per=(6, 6), k=k, drafts=6, seed=38)
     bad = {0: int(c.start[0]) + 2, 1: 85}
     c.pos[6:] = [80, 81, 84, 85, 86, 89]
     if k:
@@ -532,18 +534,33 @@ def test_values_seen_by_some(e4m3, k):
     out, lse = c.run(check=False)
     hit = [i for i in range(c.n) if bad[c.seq[i]] in c.sees(i)]
     assert 0 < len(hit) < c.n
-    o = out.double().view(c.n, 2, 3, 128)
+    o = out.double().view(c.n, 2, G, 128)
     for i in range(c.n):
         where = ~torch.isfinite(o[i])
         if i in hit:
-            assert bool(where[1, :, 5].all()) and bool(where[0, :, 64].all()) and int(where.sum()) == 6
+            assert bool(where[1, :, 5].all()) and bool(where[0, :, 64].all()) and int(where.sum()) == 2 * G
         else:
             assert not bool(where.any())
     c.check(out, lse, only=[i for i in range(c.n) if i not in hit])
 
 
-def test_a_nan_key_reaches_its_reader_only():
-    c = Case(False, 128, 1, 2, lens=(70,), per=(3,), drafts=3, seed=39)
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("G", [3, 12])
+def test_many_values_seen_by_some(e4m3, G):
+    """More non-finite values in one chunk than are handled at a time: whole rows of a drafted branch."""
+    c = Case(e4m3, 128, 1, G, lens=(70,), per=(5,), drafts=5, seed=45)
+    c.mask.copy_(ints([[1], [3], [7], [9], [17]]))
+    at = int(c.start[0])
+    for j in (1, 2):
+        c.v[0, at + j] = 0x7F if e4m3 else math.nan
+    out, lse = c.run(check=False)
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(out[2]).all())
+    c.check(out, lse, only=[0, 3, 4])
+
+
+@pytest.mark.parametrize("G", [2, 12])
+def test_a_nan_key_reaches_its_reader_only(G):
+    c = Case(False, 128, 1, G, lens=(70,), per=(3,), drafts=3, seed=39)
     c.mask.copy_(ints([[1], [3], [5]]))
     c.k[0, int(c.start[0]) + 1, 0, 7] = math.nan
     out, lse = c.run(check=False)
@@ -552,19 +569,98 @@ def test_a_nan_key_reaches_its_reader_only():
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
-def test_large_and_negative_logits(e4m3):
+@pytest.mark.parametrize("G", [3, 20])
+def test_large_and_negative_logits(e4m3, G):
     for scale in (8.0, -0.3, 1e-6, 0.0):
-        c = Case(e4m3, 64, 2, 3, lens=(400, 90), per=(2, 2), seed=40, spread=0.2)
+        c = Case(e4m3, 64, 2, G, lens=(400, 90), per=(2, 2), seed=40, spread=0.2)
         c.run(scale=scale)
 
 
-def test_scales_of_very_different_size():
+def test_logits_of_minus_infinity():
+    """A visible token whose logit is -inf weighs nothing; alone, it leaves nothing."""
+    c = Case(False, 128, 1, 1, lens=(200, 1), per=(1, 1), seed=43)
+    for i, t in ((0, 77), (0, 3), (1, 0)):
+        e = int(c.q[i, 0].float().abs().argmax())
+        c.k[i, t, 0, e] = -math.inf if float(c.q[i, 0, e]) > 0 else math.inf
+    out, lse = c.run(check=False)
+    assert not bool(out[1].any()) and float(lse[1]) == -math.inf
+    keep = [t for t in range(200) if t not in (3, 77)]
+    s = (c.k[0, keep, 0].double() @ c.q[0, 0].double()) * 128 ** -0.5
+    assert abs(float(lse[0, 0]) - float(torch.logsumexp(s, 0))) < 1e-4
+    want = torch.softmax(s, 0) @ c.v[0, keep, 0].double()
+    # as in the module's bound, |v| < 6 and the weights' sum 1
+    assert float((out[0, 0].double() - want).abs().max()) < 6 * 2 * BF16
+
+
+@pytest.mark.parametrize("G", [3, 20, 40])
+@pytest.mark.parametrize("k", [0, 64])
+def test_queries_of_any_magnitude(G, k):
+    """e4m3 caches meet f16 queries scaled by a power of two: the size of a query does not matter, and a row with an
+    infinity leaves the others alone."""
+    c = Case(True, 128, 1, G, lens=(150,), per=(2,), k=k, seed=44)
+    want, wl = c.run()
+    c.q.mul_(2.0 ** 100)
+    out, lse = c.run(scale=128 ** -0.5 * 2.0 ** -100, check=False)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    c.q.mul_(2.0 ** -100).mul_(2.0 ** -100)            # (2^-200 is not an fp32 number)
+    out, lse = c.run(scale=128 ** -0.5 * 2.0 ** 100, check=False)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    c.q.mul_(2.0 ** 100)
+    c.q[1, 1, 3] = math.inf
+    out, lse = c.run(check=False)
+    c.check(out, lse, only=[0])
+    assert torch.equal(out[1, 2], want[1, 2]) and not bool(torch.isfinite(out[1, 1].float()).all())
+
+
+@pytest.mark.parametrize("G", [4, 24])
+def test_scales_of_very_different_size(G):
     """e4m3 rows whose scales span many orders, zero among them."""
-    c = Case(True, 128, 2, 4, lens=(500, 90), per=(2, 2), k=80, seed=41, spread=6.0)
+    c = Case(True, 128, 2, G, lens=(500, 90), per=(2, 2), k=80, seed=41, spread=6.0)
     c.ks.clamp_(max=0.02)
     c.vs[:, ::7] = 0.0
     c.run()
     c.topk = None
+    c.run()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("G,per", [(1, (37, 1, 1, 1)), (8, (60, 1, 0, 2))])
+def test_uneven_batches(e4m3, G, per):
+    """More tiles than an even spread of the queries has."""
+    c = Case(e4m3, 128, 2, G, lens=(300, 64, 33, 100), per=per, seed=46, causal=True)
+    c.poison()
+    c.run()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_more_queries_than_one_scan(e4m3):
+    """Runs of queries beyond the first 1024 of a batch, one cut there."""
+    c = Case(e4m3, 64, 1, 2, lens=(20,) * 600, per=(2,) * 600, seed=47, slack=0)
+    out, lse = c.run(check=False)
+    c.check(out, lse, only=list(range(0, 40)) + list(range(1000, 1060)) + list(range(1180, 1200)))
+    c = Case(e4m3, 64, 1, 4, lens=(700, 900), per=(500, 800), seed=48, causal=True, slack=0)
+    out, lse = c.run(check=False)
+    c.check(out, lse, only=list(range(0, 1300, 37)) + list(range(1015, 1035)) + [1299])
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("k", [0, 30])
+def test_large_drafts(e4m3, G, k):
+    c = Case(e4m3, 64, 1, G, lens=(90, 40), per=(7, 2), k=k, drafts=1024, seed=49)
+    g = torch.Generator().manual_seed(1)
+    c.mask.copy_(torch.randint(-2 ** 31, 2 ** 31, c.mask.shape, generator=g).to(torch.int32))
+    c.poison()
+    c.run()
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3,d", TYPES)
+def test_long_prefixes_of_many_rows(e4m3, d):
+    """Shares of a long prefix, joined through the workspace."""
+    c = Case(e4m3, d, 1, 6, lens=(9000, 5000), per=(5, 4), drafts=5, seed=55)
+    c.poison()
     c.run()
 
 
