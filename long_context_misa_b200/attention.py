@@ -407,3 +407,34 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
           None if draft is None else draft._p, out.data_ptr(), None if lse is None else lse.data_ptr(),
           None if buf is None else buf.data_ptr(), need)
     return out if lse is None else (out, lse)
+
+
+class SparseAttention:
+    """The attention of a decode step around MISA-dagger (see misa.MisaDaggerDecode).
+
+    ``before`` rotates the rows of ``rotate`` with ``rope`` (up to four (x, pos, out) triples in one launch: the
+    step's index queries, its new index keys, its attention queries) and writes new_k, new_v
+    [n_seq][1][H_kv][d] at new_pos, the keys rotated by ``kv_rope``; ``after`` attends over the step's top-k.
+    All buffers are the caller's or allocated here once; out [n_q][H][d] and lse [n_q][H] hold the step's result.
+    """
+
+    def __init__(self, kv: KVCache, queries: AttentionQueries, new_k: torch.Tensor, new_v: torch.Tensor,
+                 new_pos: torch.Tensor, k: int, rope: Optional[Rope] = None, rotate: Sequence = (),
+                 kv_rope: Optional[Rope] = None):
+        if rotate and rope is None:
+            raise ValueError("rotate needs a rope")
+        self.kv, self.queries, self.new_k, self.new_v, self.new_pos = kv, queries, new_k, new_v, new_pos
+        self.rope, self.rotate, self.kv_rope = rope, list(rotate), kv_rope
+        dev = kv.device
+        self.out = torch.empty_like(queries.q)
+        self.lse = torch.empty((queries.n_q, queries.H), dtype=torch.float32, device=dev)
+        self.ws = Workspace(dev)
+        self.ws.get(attend_workspace_bytes(kv, queries, int(k)))
+
+    def before(self, stream=None) -> None:
+        if self.rotate:
+            apply_rope(self.rope, self.rotate, stream=stream)
+        append_kv(self.kv, self.new_k, self.new_v, self.new_pos, rope=self.kv_rope, stream=stream)
+
+    def after(self, topk: torch.Tensor, stream=None) -> torch.Tensor:
+        return attend(self.kv, self.queries, topk=topk, out=self.out, lse=self.lse, ws=self.ws, stream=stream)[0]

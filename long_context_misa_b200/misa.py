@@ -381,6 +381,11 @@ class MisaDaggerDecode:
     new_keys  [n_seq][1][128] (cache dtype), new_scale [n_seq][1] (e4m3 only)
     and new_pos [n_seq] are device tensors the caller refills between steps
     (new_pos is normally q_pos).
+
+    attention (an attention.SparseAttention) puts the attention around the
+    selection into the same step: positions rotated and the new tokens' keys
+    and values written before it, attention over the top k after it, its
+    result in attention.out.
     """
 
     # kernels of one step when the batch runs fused (decode shapes whose
@@ -391,8 +396,9 @@ class MisaDaggerDecode:
     LAUNCHES = 3
 
     def __init__(self, cache: KeyCache, qs: Queries, h: int, k_prime: int, k: int, new_keys: torch.Tensor,
-                 new_scale: Optional[torch.Tensor], new_pos: torch.Tensor):
+                 new_scale: Optional[torch.Tensor], new_pos: torch.Tensor, attention=None):
         dev = qs.q.device
+        self.attention = attention
         self.cache, self.qs, self.h, self.k_prime, self.k = cache, qs, h, k_prime, k
         self.new_keys, self.new_scale, self.new_pos = new_keys, new_scale, new_pos
         self.heads = torch.empty(qs.n_q, h, dtype=torch.int32, device=dev)
@@ -403,8 +409,12 @@ class MisaDaggerDecode:
         self.graph = None
 
     def run(self, stream=None) -> torch.Tensor:
+        if self.attention is not None:
+            self.attention.before(stream)
         dagger_decode(self.cache, self.qs, self.new_keys, self.new_scale, self.new_pos, self.h, self.k_prime, self.k,
                       heads=self.heads, topk=self.topk, ws=self.ws, stream=stream)
+        if self.attention is not None:
+            self.attention.after(self.topk, stream)
         return self.topk
 
     def capture(self) -> "MisaDaggerDecode":

@@ -803,3 +803,60 @@ def test_a_run_of_them_together():
     # the same tokens and bits in another order of sums: within both calls' bounds of one exact value
     assert float((out.double() - tree_out[[4, 5]].double()).abs().max()) <= 4 * BF16 * float(out.abs().max())
     assert kv.device_status() == 0
+
+
+def test_decode_step_with_its_attention():
+    """MisaDaggerDecode with the attention in it: the separate calls' results, run, captured and replayed; the
+    selection is what the step without it selects."""
+    from long_context_misa_b200 import inputs as G
+    wl = G.WORKLOADS["tiny_decode"].scaled(k_prime=1024)
+    inp = G.make_inputs(wl, 0)
+    cache, qs = M.device_inputs(inp)
+    n, L, H_kv, H, d = wl.n_seq, cache.L_cap, 4, 16, 128
+    g = gen(70)
+    pos = ints((inp.seq_len - 1).tolist())
+    cache.seq_len.copy_(pos)
+    M.pool_keys(cache)
+    last = torch.stack([cache.keys[s, int(pos[s]):int(pos[s]) + 1] for s in range(n)]).clone()
+    plain = M.MisaDaggerDecode(cache, qs, wl.h, wl.k_prime, wl.k, last, None, pos)
+    plain.run()
+    # the step's raw rows, unrotated, as projections give them
+    r = A.Rope(64, layout="interleaved", base=500000.0)
+    raw_iq = qs.q.clone().view(torch.bfloat16)
+    raw_q = randn(g, qs.n_q, H, d).bfloat16()
+    q = torch.empty_like(raw_q)
+    kv = A.KVCache.empty(n, L, H_kv, d, True)
+    hist = [randn(g, n, L - 1, H_kv, d).bfloat16() for _ in range(2)]
+    A.append_kv(kv, *hist, ints([0] * n), rope=r)
+    kv.seq_len.copy_(pos)
+    new = [randn(g, n, 1, H_kv, d).bfloat16() for _ in range(2)]
+    aq = A.AttentionQueries(q, qs.q_seq, qs.q_pos)
+
+    def sparse(rotate):
+        return A.SparseAttention(kv, aq, *new, pos, wl.k, rope=r, rotate=rotate, kv_rope=r)
+    # attention queries rotated only: the selection does not change
+    step = M.MisaDaggerDecode(cache, qs, wl.h, wl.k_prime, wl.k, last, None, pos, attention=sparse([(raw_q, qs.q_pos, q)]))
+    step.run()
+    assert torch.equal(step.topk, plain.topk)
+    want = A.attend(kv, aq, topk=plain.topk, with_lse=True)
+    assert torch.equal(step.attention.out, want[0]) and torch.equal(step.attention.lse, want[1])
+    # index queries rotated as well, the step captured and replayed on new rows
+    step = M.MisaDaggerDecode(cache, qs, wl.h, wl.k_prime, wl.k, last, None, pos,
+                              attention=sparse([(raw_iq, qs.q_pos, qs.q.view(torch.bfloat16)), (raw_q, qs.q_pos, q)]))
+    step.run()
+    step.capture()
+    for i in range(2):
+        raw_iq.copy_(randn(g, *raw_iq.shape)), raw_q.copy_(randn(g, *raw_q.shape)), new[0].copy_(randn(g, *new[0].shape))
+        step.replay()
+        torch.cuda.synchronize()
+        c = Case.__new__(Case)
+        c.e4m3, c.d, c.H_kv, c.G, c.lens, c.draft, c.cap = True, d, H_kv, H // H_kv, tuple(inp.seq_len.tolist()), None, L
+        c.k, c.v, c.ks, c.vs, c.kv = kv.k, kv.v, kv.k_scale, kv.v_scale, kv
+        c.seq, c.pos, c.n, c.q, c.topk = qs.q_seq.tolist(), qs.q_pos.tolist(), qs.n_q, q, step.topk
+        check_rope(q, raw_q, qs.q_pos, r)
+        check_rope(qs.q.view(torch.bfloat16), raw_iq, qs.q_pos, r)
+        assert torch.equal(step.topk, M.dagger_topk(cache, qs, step.heads, wl.k_prime, wl.k))
+        c.check(step.attention.out, step.attention.lse)
+    assert kv.device_status() == 0 and cache.device_status() == 0
+    with pytest.raises(ValueError):
+        A.SparseAttention(kv, aq, *new, pos, wl.k, rotate=[(raw_q, qs.q_pos, q)])
