@@ -152,7 +152,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
   __shared__ Shared sh;
   __shared__ Scales<FP8> scales;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t *smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+  const uint32_t pad = (1024u - (smem_addr(raw_smem) & 1023u)) & 1023u;
+  uint32_t dyn;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
+  if (pad + F::SMEM - 1024 > dyn) {  // a layout and an allocation that disagree
+    if (tid == 0) flag(c, MISA_DEV_SMEM_LAYOUT);
+    return;
+  }
+  uint8_t *smem = raw_smem + pad;
   uint8_t *q_s = smem, *k_s = smem + F::QTILE, *v_s = k_s + NK * TILE, *raw_s = v_s + NV * TILE;
   const int G = a.H / c.H_kv, hk = blockIdx.y, Z = split.Z;
   volatile int *abort = &sh.abort;
