@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       mbar_init(&sh.done, 1), mbar_init(&sh.joined, 256);
       fence_mbar_init();
       sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff, sh.q_max = 0;
+      sh.n_bad[0] = sh.n_bad[1] = 0;
     }
     __syncthreads();
     if (tid < M) {
@@ -511,6 +512,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       float y_ref = NOTHING, l_sum = 0.f;  // base-2 reference of O and of the sum, and the sum
       bool ok = true;
       int scans = 0;
+      // the row's mask of the first drafted chunk's half, read ahead
+      uint32_t drafted[W];
+      auto draft_word = [&](int d0) -> uint32_t {
+        uint32_t m = !LIST && r < n_rows && my_len >= 0 && d0 < n_draft
+                         ? a.draft_mask[(int64_t)my_query * words + (d0 >> 5)]
+                         : 0u;
+        if (n_draft - d0 < 32) m &= n_draft > d0 ? (1u << (n_draft - d0)) - 1u : 0u;
+        return m;
+      };
+#pragma unroll
+      for (int w = 0; w < W; ++w) drafted[w] = draft_word(g * HALF + w * 32);
       // bounded waits of a whole warp (its tensor-memory accesses need all lanes)
       auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, c)) != 0; };
       auto meet = [&]() {  // the 128 threads of the set
@@ -546,15 +558,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           for (int w = 0; w < W; ++w) {
             uint32_t v = sh.have[slot][W * g + w];
             if (!LIST && r < n_rows) {  // (nobody reads the other rows)
-              if (my_len < 0) {
-                v = 0u;
-              } else {
-                const int d0 = (ck - c1) * TOK + g * HALF + w * 32;
-                uint32_t m = d0 < n_draft ? a.draft_mask[(int64_t)my_query * words + (d0 >> 5)] : 0u;
-                if (n_draft - d0 < 32) m &= n_draft > d0 ? (1u << (n_draft - d0)) - 1u : 0u;
-                if (m & ~v) flag(c, MISA_DEV_BAD_POSITION);
-                v &= m;
-              }
+              const uint32_t m = ck == c1 ? drafted[w] : draft_word((ck - c1) * TOK + g * HALF + w * 32);
+              if (m & ~v) flag(c, MISA_DEV_BAD_POSITION);
+              v &= m;
             }
             see[w] = v;
             masked |= v != 0xffffffffu;
@@ -647,21 +653,26 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
 #pragma unroll
         for (int i = 0; i < HALF / 2; i += 16) st16(ts + i, reinterpret_cast<const uint32_t(&)[16]>(pk[i]));
         // ---- values that some rows must not see: NaN and infinities there
-        // would reach them as 0 * NaN.  They are taken out of the tile and
-        // added to O in the rows that see them (a weight is positive) ----
-        if (!LIST && (ck >= c1 || (ck + 1) * TOK > min_len)) {
+        // would reach them as 0 * NaN.  What lies behind the longest prefix is
+        // cleared; what some rows see is taken out of the tile and added to O
+        // in those rows (a weight is positive) ----
+        const int first = ck * TOK + g * HALF;  // the half's first token
+        if (stretch ? first + HALF > min_len : !LIST) {
           ok = wait(&sh.vfull[j % NV], (j / NV) & 1);
-          if (ok && j > 0) ok = wait(&sh.pvdone[g], (j - 1) & 1);
-          umma::fence_after();
           uint8_t *vt = v_s + (j % NV) * TILE;
           constexpr uint32_t EXP = FP8 ? 0x7c00u : 0x7f80u;
-          int left = 0;
-          while (ok) {
-            if (!(ok = meet())) break;
-            if (r == 0) sh.n_bad[g] = 0;
-            if (!(ok = meet())) break;
-            for (int p = 0; p < (r < HALF ? DH / 8 : 0); ++p) {
-              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(g * HALF + r, p, BLK));
+          if (stretch && r < HALF && first + r >= max_len)
+            for (int p = 0; p < DH / 8; ++p)
+              *reinterpret_cast<uint4 *>(vt + tile_at(g * HALF + r, p, BLK)) = make_uint4(0u, 0u, 0u, 0u);
+          // rows of the half that some see and some do not: [r0, r1), their
+          // pieces dealt to the set's threads
+          const int r0 = stretch ? max(min_len - first, 0) : 0;
+          const int r1 = min(stretch ? max_len - first : n_draft - (ck - c1) * TOK - g * HALF, HALF);
+          bool some = ok && r0 < r1;  // (the same in the whole set)
+          while (some) {
+            for (int x = r0 * (DH / 8) + r; x < r1 * (DH / 8); x += 128) {
+              const int row = x / (DH / 8), p = x % (DH / 8);
+              uint16_t *e = reinterpret_cast<uint16_t *>(vt + tile_at(g * HALF + row, p, BLK));
               const uint4 q = *reinterpret_cast<const uint4 *>(e);
               const uint32_t w[4] = {q.x, q.y, q.z, q.w};
               bool any = false;
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
                 if ((bits & EXP) != EXP) continue;
                 const int at = atomicAdd(&sh.n_bad[g], 1);
                 if (at >= BAD) continue;  // the next round's
-                sh.bad_at[g][at] = make_int2(r, p * 8 + i);
+                sh.bad_at[g][at] = make_int2(row, p * 8 + i);
                 const uint32_t mant = bits & (FP8 ? 0x3ffu : 0x7fu);
                 sh.bad_val[g][at] =
                     mant ? __int_as_float(0x7fffffff) : __int_as_float((bits & 0x8000u) ? 0xff800000u : 0x7f800000u);
@@ -681,8 +692,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               }
             }
             if (!(ok = meet())) break;
-            left = sh.n_bad[g];
-            for (int i = 0; i < min(left, BAD); ++i) {
+            const int found = sh.n_bad[g];
+            if (found == 0) break;
+            if (j > 0 && !(ok = wait(&sh.pvdone[g], (j - 1) & 1))) break;  // O may change now
+            umma::fence_after();
+            for (int i = 0; i < min(found, BAD); ++i) {
               const int2 at = sh.bad_at[g][i];
               const uint32_t sw = at.x < 32 ? see[0] : see[1];
               const uint32_t ov = ld1(to + at.y);
@@ -690,7 +704,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               st1(to + at.y, mine ? __float_as_uint(__uint_as_float(ov) + sh.bad_val[g][i]) : ov);
               st_wait();
             }
-            if (left <= BAD) break;
+            if (!(ok = meet())) break;
+            if (r == 0) sh.n_bad[g] = 0;
+            if (!(ok = meet())) break;
+            some = found > BAD;
           }
           umma::fence_proxy_async();
           if (!ok) break;
