@@ -416,6 +416,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           cp_async_commit();
           return true;
         };
+        // the 8 lanes of a row store their even or their odd halves first, so
+        // that a store of theirs meets every bank once
+        const int odd = (pc * 2) >> 3 & 1;
         bool ok = true;
         for (int j = 0; j < NR - 1 && ok; ++j) ok = bring(j);
         for (int j = 0; j < n && ok; ++j) {
@@ -430,9 +433,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             const uint4 v = *reinterpret_cast<const uint4 *>(from + i * (GROUP * 16));
             const int r = r0 + i * RSTEP;
             uint32_t w[8];
-            widen(v.x, w[0], w[1]), widen(v.y, w[2], w[3]), widen(v.z, w[4], w[5]), widen(v.w, w[6], w[7]);
-            *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc, BLK)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc + 1, BLK)) = make_uint4(w[4], w[5], w[6], w[7]);
+            widen(odd ? v.z : v.x, w[0], w[1]), widen(odd ? v.w : v.y, w[2], w[3]);
+            widen(odd ? v.x : v.z, w[4], w[5]), widen(odd ? v.y : v.w, w[6], w[7]);
+            *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc + odd, BLK)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(dst + tile_at(r, 2 * pc + 1 - odd, BLK)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
           mbar_arrive(&sh.rawempty[vals][j % NR]);
           umma::fence_proxy_async();
