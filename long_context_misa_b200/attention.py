@@ -118,11 +118,14 @@ def _call(fn, device, stream, *args) -> None:
         _m._check(st)
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _allocating(stream):
     """Where a call runs on a given stream, what it allocates belongs to that stream: its memory is not handed out
     again before the call is done with it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     return torch.cuda.stream(stream)
@@ -221,6 +224,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale, self.seq_len = k, v, k_scale, v_scale, seq_len
         self.dtype = MISA_KEY_FP8_E4M3 if fp8 else MISA_KEY_BF16
         self.device = k.device
+        self._shape = (self.n_seq, self.L_cap, self.H_kv, self.d, self.dtype)
         self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=k.device)
         _ints(self.status, 1, "status", k.device)
         self._s = misa_kv(_m._ptr(k), _m._ptr(v), _m._ptr(k_scale), _m._ptr(v_scale), _m._ptr(seq_len),
@@ -280,18 +284,19 @@ def read_kv(kv: KVCache, seq: torch.Tensor, tok: torch.Tensor, k_out: Optional[t
     n, k = tok.shape
     device, shape = kv.device, (n, k, kv.H_kv, kv.d)
     _ints(seq, n, "seq", device), _ints(tok, n * k, "tok", device)
+    for t in (k_out, v_out):
+        if t is not None:
+            if t.dtype not in _BF16:
+                raise TypeError(f"outputs must be bf16, got {t.dtype}")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"outputs must be contiguous {shape}, got {tuple(t.shape)}")
+            _on(t, device, "output")
     if k_out is None or v_out is None:
         with _allocating(stream):
             if k_out is None:
                 k_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
             if v_out is None:
                 v_out = torch.empty_like(k_out)
-    for t in (k_out, v_out):
-        if t.dtype not in _BF16:
-            raise TypeError(f"outputs must be bf16, got {t.dtype}")
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"outputs must be contiguous {shape}, got {tuple(t.shape)}")
-        _on(t, device, "output")
     _call(_lib.misa_read_kv, device, stream, kv._p, seq.data_ptr(), tok.data_ptr(), n, k, k_out.data_ptr(),
           v_out.data_ptr())
     return k_out, v_out
@@ -310,6 +315,7 @@ class AttentionQueries:
         self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(self.d)
         # one element in the shape of an lse: torch allocates like a tensor in half the time of a new one
         self._lse = torch.empty((1, 1), dtype=torch.float32, device=q.device).expand(self.n_q, self.H)
+        self._need = {}  # workspace bytes by the shapes that decide them
         self._s = misa_attend_queries(_m._ptr(q), _m._ptr(q_seq), _m._ptr(q_pos), self.n_q, self.H, self.scale)
         self._p = ctypes.byref(self._s)
 
@@ -383,7 +389,22 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
                              f"queries and {kv.n_seq} sequences")
         _on(draft.mask, dev, "draft")
         n_draft = draft.n
-    need = _lib.misa_attend_workspace_bytes(kv._p, qs._p, k, n_draft)
+    if out is not None:
+        if out.dtype not in _BF16:
+            raise TypeError(f"out must be bf16, got {out.dtype}")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
+        _on(out, dev, "out")
+    if lse is not None:
+        if lse.dtype is not torch.float32:
+            raise TypeError(f"lse must be float32, got {lse.dtype}")
+        if lse.shape != (qs.n_q, qs.H) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{qs.n_q}][{qs.H}], got {tuple(lse.shape)}")
+        _on(lse, dev, "lse")
+    key = (k, n_draft, kv._shape)
+    need = qs._need.get(key)
+    if need is None:
+        need = qs._need[key] = attend_workspace_bytes(kv, qs, k, n_draft)
     buf = None
     with _allocating(stream):
         if out is None:
@@ -392,17 +413,6 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
             lse = torch.empty_like(qs._lse, memory_format=torch.contiguous_format)
         if need:
             buf = (ws or Workspace(dev)).get(need)
-    if out.dtype not in _BF16:
-        raise TypeError(f"out must be bf16, got {out.dtype}")
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
-    _on(out, dev, "out")
-    if lse is not None:
-        if lse.dtype is not torch.float32:
-            raise TypeError(f"lse must be float32, got {lse.dtype}")
-        if lse.shape != (qs.n_q, qs.H) or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous [{qs.n_q}][{qs.H}], got {tuple(lse.shape)}")
-        _on(lse, dev, "lse")
     _call(_lib.misa_attend, dev, stream, kv._p, qs._p, None if topk is None else topk.data_ptr(), k,
           None if draft is None else draft._p, out.data_ptr(), None if lse is None else lse.data_ptr(),
           None if buf is None else buf.data_ptr(), need)
