@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         km[y] = FP8 ? ss[g + 8 * y] * mul : mul;
         vs[y] = FP8 ? ss[CH + g + 8 * y] : 1.f;
       }
-      float p[NR][4 * MTL], w[NR][4 * MTL];
+      float p[NR][4 * MTL], w[NR][4 * MTL], l_new[NR][2];
       auto logit = [&](auto m, float v, int n, int x, int y) {
         return m.value && !(((LIST ? have : vis[n][x]) >> (g + 8 * y)) & 1u) ? NEG_INF : v;
       };
@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x) {
+            l_new[n][x] = 0.f;
 #pragma unroll
             for (int y = 0; y < 2 * MTL; ++y) {
               const int e = 2 * y + x;
@@ -448,8 +449,11 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
               w[n][e] = FP8 ? p[n][e] * vs[y] : p[n][e];
               // (rows gathered for others may hold any scale)
               if (FP8 && !LIST && m.value && v == NEG_INF) w[n][e] = 0.f;
+              l_new[n][x] += p[n][e];
               top = fmaxf(top, w[n][e]);
             }
+            if (FP8 && l_new[n][x] > SUM_MAX) top = 2.f * LAZY;
+          }
         return __any_sync(0xffffffffu, top > LAZY);
       };
       for (bool again = false;; again = true) {
@@ -477,13 +481,12 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       }
       uint32_t pb[NR][2 * MTL];
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+      for (int n = 0; n < NR; ++n) {
+        l_sum[n][0] += l_new[n][0], l_sum[n][1] += l_new[n][1];
 #pragma unroll
-        for (int y = 0; y < 2 * MTL; ++y) {
-          l_sum[n][0] += p[n][2 * y];
-          l_sum[n][1] += p[n][2 * y + 1];
+        for (int y = 0; y < 2 * MTL; ++y)
           pb[n][y] = movmatrix_trans(FP8 ? f16x2(w[n][2 * y], w[n][2 * y + 1]) : bf16x2(w[n][2 * y], w[n][2 * y + 1]));
-        }
+      }
 
       // ---- values that some rows must not see: a NaN or infinity there would
       // reach them as 0 * NaN.  Such values are taken out of the chunk and

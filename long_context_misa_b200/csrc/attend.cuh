@@ -7,6 +7,10 @@
 namespace misa {
 
 constexpr float LAZY = 256.f;  // most that a weight may reach before its reference moves
+// most that a chunk's weights may add to a row's sum before the reference moves:
+// rows of scale 0 add nothing to O, whatever they weigh (2^18 tokens of such
+// chunks still fit fp32)
+constexpr float SUM_MAX = 0x1p110f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NEG_INF = -__builtin_huge_valf();

@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             }
           }
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          return top;
+          return FP8 && sum > SUM_MAX ? 2.f * LAZY : top;
         };
         float sum = 0.f, top = LAZY + 1.f;
         if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);

@@ -623,6 +623,39 @@ def test_scales_of_very_different_size(G):
     c.run()
 
 
+@pytest.mark.parametrize("G", [2, 12, 24, 40])
+def test_values_of_scale_zero_come_first(G):
+    """Rows of scale 0 weigh in the sum although they add nothing: alone, before any other token, and with logits far
+    above every other's."""
+    c = Case(True, 128, 1, G, lens=(700,), per=(2,), k=256, seed=45)
+    c.vs[:, :400] = 0.0
+    full = c.topk.clone()
+    for n in (1, 100, 256):                            # listed tokens, nothing listed before them
+        c.topk = torch.full_like(full, -1)
+        c.topk[:, 256 - n:] = full[:, :n]              # (sorted: those of scale 0 first)
+        c.run()
+    c.topk = None
+    c.run()
+    for p in (0, 300, 450):
+        c.pos = [-1, p]
+        c.run()
+    # logits of up to +-450 (base 2); the others' weights are below 2^-200 of the sum, and come out below 2^-90
+    c.pos = [699, 699]
+    big = 300.0 / float((c.q[0].float().abs().amax() * 30))
+    c.k[0, 350] = torch.where(c.q[0, 0] >= 0, 0x7E, 0xFE).to(torch.uint8)
+    c.k[0, 450] = 0
+    c.ks[0, 350] = big
+    c.q[:] = c.q[:1, :1].abs() * torch.sign(c.q[:1, :1])
+    for t in (None, ints([[450, 350], [350, 450]])):
+        c.topk = t
+        out, lse = c.run(check=False)
+        (kc, ks), _ = c.rows64(0)
+        s = torch.einsum("d,td->t", c.q[0, 0].double(), kc[:, 0] * ks) * 128 ** -0.5
+        assert float(s.amax()) > 200 + float(s[s < s.amax()].amax())
+        assert bool((out.float().abs() <= 2.0 ** -90).all())
+        assert bool(((lse.double() - s.amax()).abs() <= 2.0 ** -14 * s.amax()).all())
+
+
 @pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("G,per", [(1, (37, 1, 1, 1)), (8, (60, 1, 0, 2))])
 def test_uneven_batches(e4m3, G, per):
