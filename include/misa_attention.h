@@ -39,8 +39,8 @@ extern "C" {
  * Attention cache of n_seq sequences.
  *   k, v     [n_seq][L_cap][H_kv][d]  bf16 bit patterns or e4m3 codes, 16-byte
  *                                     aligned
- *   k_scale, v_scale [n_seq][L_cap][H_kv] fp32 dequantisation scales >= 0 of
- *                                     each row of d elements; NULL for bf16,
+ *   k_scale, v_scale [n_seq][L_cap][H_kv] fp32 dequantisation scales of 0 to
+ *                                     2^100 of each row of d elements; NULL for bf16,
  *                                     non-NULL for e4m3
  *   seq_len  [n_seq]                  int32 committed tokens per sequence
  *   status   [1] uint32 or NULL       device error bits (MISA_DEV_*)
@@ -108,7 +108,8 @@ MISA_API misa_status misa_rope_phases(uint64_t *phases, int32_t rot, double base
  * A tensor of rows to rotate: x and y are bf16 bit patterns [n][H][d] with the
  * given strides in elements between rows and between heads (the d elements of
  * a head are consecutive); pos [n] int32, any value, is each row's position.
- * y may be x with equal strides (in place); other overlaps are not allowed.
+ * y may be x with equal strides (in place); other overlaps are not allowed,
+ * rows of y that share memory and groups that write the same rows among them.
  */
 typedef struct {
   const uint16_t *x;
@@ -128,8 +129,9 @@ typedef struct {
  * 16-byte accesses; others are handled element by element.
  * Errors: MISA_ERR_INVALID for NULL pointers, n or H < 0, rot odd or outside
  * [2, d - first], first < 0, an unknown layout, a non-finite amplitude, a
- * group count outside [1, MISA_MAX_ROPE_GROUPS]; MISA_ERR_UNSUPPORTED for
- * d > 1024.
+ * group count outside [1, MISA_MAX_ROPE_GROUPS], in place with other strides,
+ * rows of y whose strides let them meet, groups of which one starts where
+ * another writes; MISA_ERR_UNSUPPORTED for d > 1024.
  */
 MISA_API misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups, int32_t n_groups,
                                      misa_stream stream);
@@ -160,11 +162,14 @@ typedef struct {
  * sequence s untouched; a write past L_cap skips the sequence and sets
  * MISA_DEV_APPEND_RANGE.  Writing the same rows again is idempotent, so the
  * drafted tokens that are accepted are written again at their places.
+ * new_pos may be seq_len itself (the tokens go behind what is there); it is
+ * then updated by a second launch, after the write that reads it.
  * A row that holds a NaN or infinity keeps it as far as its type can (NaN
  * codes in e4m3).
  * Errors: those of the cache and rope; MISA_ERR_INVALID for count < 1 or
  * above L_cap, NULL new_kv/k/v/new_pos, rows not on 16 bytes (pointers, and
- * strides not multiples of 8).
+ * strides not multiples of 8), commit with a new_pos that overlaps seq_len
+ * without being it.
  */
 MISA_API misa_status misa_append_kv(const misa_kv *kv, const misa_new_kv *new_kv, const int32_t *new_pos,
                                     int32_t count, const misa_rope *rope, const int32_t *rope_pos, int32_t commit,
@@ -180,7 +185,7 @@ MISA_API misa_status misa_append_kv(const misa_kv *kv, const misa_new_kv *new_kv
  *   them may be NULL
  * Tokens at and beyond seq_len (drafted ones) are read as they are.
  * Errors: those of the cache; MISA_ERR_INVALID for n < 0, k < 1, NULL seq or
- * tok, or both outputs NULL; MISA_ERR_UNSUPPORTED for k > MISA_MAX_L.
+ * tok, both outputs NULL or overlapping; MISA_ERR_UNSUPPORTED for k > MISA_MAX_L.
  */
 MISA_API misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *tok, int32_t n, int32_t k,
                                   uint16_t *k_out, uint16_t *v_out, misa_stream stream);
@@ -236,14 +241,16 @@ typedef struct {
  * sequence or position is outside the cache gets nothing or the clamped
  * prefix and sets MISA_DEV_BAD_POSITION.
  * Numbers: products of the stored values with fp32 sums; softmax statistics
- * in fp32; the weights exp(s_t - max) are rounded to bf16 (bf16 caches) or,
- * with v_scale folded in, to f16 (e4m3 caches, whose codes are exact in f16)
- * before they meet the values.
+ * in fp32.  bf16 caches: the weights exp(s_t - ref), ref a running maximum of
+ * s_t, are rounded to bf16 before they meet the values.  e4m3 caches: the
+ * codes are exact in f16; q is scaled by one power of two per group of rows
+ * and exp(s_t - ref) v_scale_t, ref a running maximum of s_t + ln v_scale_t
+ * (v_scale_t held within 2^-100 and 2^100 there), is rounded to f16.
  * Workspace: misa_attend_workspace_bytes(kv, qs, k, draft ? draft->n : 0),
  * 16-byte aligned.  Results do not depend on what it held.
  * Errors: those of the cache; MISA_ERR_INVALID for NULL q/q_seq/q_pos/out,
  * n_q outside [0, 65535], H not a positive multiple of H_kv, a non-finite
- * scale, k < 1 with a list or k != 0 without one, a draft with NULL pointers
+ * scale, out that overlaps q, k < 1 with a list or k != 0 without one, a draft with NULL pointers
  * or n < 1; MISA_ERR_UNSUPPORTED for H > MISA_MAX_H, k > MISA_MAX_L, draft->n
  * > MISA_MAX_DRAFT; MISA_ERR_WORKSPACE for a short workspace.
  */

@@ -108,8 +108,8 @@ def _on(t: torch.Tensor, device, what: str) -> None:
 def _call(fn, device, stream, *args) -> None:
     """fn(*args, stream) with `device` current; the default is the device's current stream."""
     if device.type != "cuda":
-        st = fn(*args, None if stream is None else _m._stream(stream))
-    elif device.index == torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}: the kernels need a CUDA device")
+    if device.index == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _m._stream(stream))
     else:
         with torch.cuda.device(device):
@@ -169,7 +169,7 @@ def apply_rope(rope: Rope, rows: Sequence[Tuple[torch.Tensor, torch.Tensor, torc
     """Rotate up to four tensors in one launch.
 
     rows: (x, pos, out) triples; x and out are bf16 (or bf16 bits) [n][H][d] with consecutive elements along d and
-    any other strides, out may be x itself; pos is int32 [n].
+    any other strides, out may be x itself; pos is int32 [n].  Rows of one out, and the triples, must not meet.
     """
     if not 1 <= len(rows) <= MAX_ROPE_GROUPS:
         raise ValueError(f"apply_rope takes 1 to {MAX_ROPE_GROUPS} tensors, got {len(rows)}")
@@ -253,6 +253,7 @@ def append_kv(kv: KVCache, new_k: torch.Tensor, new_v: torch.Tensor, new_pos: to
               stream=None) -> None:
     """Write new_k, new_v (bf16 [n_seq][count][H_kv][d], consecutive along d) at new_pos [n_seq], the keys rotated
     by rope at rope_pos [n_seq][count] (default: the positions written) and quantised to the cache's type.
+    new_pos may be kv.seq_len itself: the tokens go behind what is there.
     commit=False leaves seq_len (drafted tokens)."""
     shape = new_k.shape
     if new_k.dtype not in _BF16 or new_v.dtype not in _BF16:

@@ -27,6 +27,9 @@ struct RopeView {
   float amplitude;
 };
 
+// Whether two arrays of int32 share memory.
+inline bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) { return a < b + nb && b < a + na; }
+
 // Heads that one thread of the rotary and cache kernels takes: `flat` threads
 // would take one each.  A thread's 8 cos and sin cost about 350 instructions,
 // as many as the memory leaves room for per 64 bytes, so a large call shares

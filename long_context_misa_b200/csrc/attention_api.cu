@@ -37,6 +37,19 @@ misa_status check_rope(const misa_rope *r, int d) {
   return MISA_OK;
 }
 
+// Whether [n][H] rows of d elements with these strides do not meet: one of the
+// two axes steps over all of the other's rows.
+bool apart(int64_t row, int n, int64_t head, int H, int d) {
+  auto size = [](int64_t x) { return x < 0 ? -x : x; };
+  const int64_t r = size(row), h = size(head);
+  const bool rows_out = (n < 2 || r >= (H < 2 ? d : h * (H - 1) + d)) && (H < 2 || h >= d);
+  const bool heads_out = (H < 2 || h >= (n < 2 ? d : r * (n - 1) + d)) && (n < 2 || r >= d);
+  return rows_out || heads_out;
+}
+
+// Whether two arrays of n 16-bit elements share memory.
+bool overlap16(const uint16_t *a, const uint16_t *b, int64_t n) { return a < b + n && b < a + n; }
+
 misa::KvView view(const misa_kv *c) {
   misa::KvView v;
   v.k = static_cast<uint8_t *>(c->k);
@@ -131,6 +144,12 @@ misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups,
     if (g.n > 0 && g.H > 0 && (!g.x || !g.y || !g.pos)) return fail(MISA_ERR_INVALID, "group %d: x/y/pos is NULL", i);
     if (g.x == g.y && (g.x_row != g.y_row || g.x_head != g.y_head))
       return fail(MISA_ERR_INVALID, "group %d: in place needs equal strides", i);
+    if (!apart(g.y_row, g.n, g.y_head, g.H, g.d)) return fail(MISA_ERR_INVALID, "group %d: rows of y overlap", i);
+    for (int j = 0; j < i; ++j) {
+      const misa_rope_rows &o = groups[j];
+      if (g.y && (g.y == o.y || g.y == o.x || g.x == o.y) && g.n > 0 && g.H > 0 && o.n > 0 && o.H > 0)
+        return fail(MISA_ERR_INVALID, "groups %d and %d: one writes what the other takes", j, i);
+    }
   }
   if (injected_failure("misa_apply_rope", &st)) return st;
   const cudaError_t e = misa::launch_rope(view(rope), groups, n_groups, stream);
@@ -145,6 +164,8 @@ misa_status misa_append_kv(const misa_kv *kv, const misa_new_kv *new_kv, const i
   if (rope && (st = check_rope(rope, kv->d)) != MISA_OK) return st;
   if (count < 1 || count > kv->L_cap) return fail(MISA_ERR_INVALID, "count=%d outside [1, L_cap=%d]", count, kv->L_cap);
   if (!new_kv || !new_kv->k || !new_kv->v || !new_pos) return fail(MISA_ERR_INVALID, "new_kv/k/v/new_pos is NULL");
+  if (commit && new_pos != kv->seq_len && misa::overlap(new_pos, kv->n_seq, kv->seq_len, kv->n_seq))
+    return fail(MISA_ERR_INVALID, "new_pos overlaps seq_len");
   if (rope_pos && !rope) return fail(MISA_ERR_INVALID, "rope_pos without rope");
   const int64_t strides[6] = {new_kv->k_seq, new_kv->k_tok, new_kv->k_head, new_kv->v_seq, new_kv->v_tok, new_kv->v_head};
   for (const int64_t x : strides)
@@ -165,6 +186,8 @@ misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *t
   if (!k_out && !v_out) return fail(MISA_ERR_INVALID, "k_out and v_out are both NULL");
   if (n > 0 && (!seq || !tok)) return fail(MISA_ERR_INVALID, "seq/tok is NULL");
   if (!aligned16(k_out) || !aligned16(v_out)) return fail(MISA_ERR_INVALID, "k_out and v_out must be 16-byte aligned");
+  if (k_out && v_out && overlap16(k_out, v_out, (int64_t)n * k * kv->H_kv * kv->d))
+    return fail(MISA_ERR_INVALID, "k_out and v_out overlap");
   if (injected_failure("misa_read_kv", &st)) return st;
   const cudaError_t e = misa::launch_read_kv(view(kv), seq, tok, n, k, k_out, v_out, stream);
   return e == cudaSuccess ? MISA_OK : cuda_fail(e, "misa_read_kv");
@@ -186,6 +209,8 @@ misa_status misa_attend(const misa_kv *kv, const misa_attend_queries *qs, const 
     return fail(MISA_ERR_INVALID, "draft n=%d, start or mask NULL", draft->n);
   if (qs->n_q > 0 && (!qs->q || !qs->q_seq || !qs->q_pos || !out))
     return fail(MISA_ERR_INVALID, "q/q_seq/q_pos/out is NULL");
+  if (qs->n_q > 0 && overlap16(qs->q, out, (int64_t)qs->n_q * qs->H * kv->d))
+    return fail(MISA_ERR_INVALID, "out overlaps q");
   if (!std::isfinite(qs->scale)) return fail(MISA_ERR_INVALID, "scale is not finite");
   if (!aligned16(qs->q) || !aligned16(out)) return fail(MISA_ERR_INVALID, "q and out must be 16-byte aligned");
   const size_t need = misa::attend_ws_bytes(view(kv), qs->n_q, qs->H, k, draft ? draft->n : 0);

@@ -154,6 +154,16 @@ __global__ void __launch_bounds__(THREADS, 5) append_kv_kernel(KvView c, misa_ne
   }
 }
 
+// seq_len where the cache's own lengths said where the tokens go: the write
+// reads them, so they change once it is done.
+__global__ void commit_kv_kernel(KvView c, const int32_t *new_pos, int count) {
+  grid_dep_sync();
+  const int s = blockIdx.x * THREADS + threadIdx.x;
+  if (s >= c.n_seq) return;
+  const int pos = new_pos[s];
+  if (pos >= 0 && (int64_t)pos + count <= c.L_cap) c.seq_len[s] = pos + count;
+}
+
 // blockIdx.z: keys or values; blockIdx.y: list; blockIdx.x: the list's
 // pieces of 8 elements, READ_PIECES of them per thread, THREADS apart: a warp
 // stores 512 contiguous bytes at a time.
@@ -216,6 +226,8 @@ __global__ void __launch_bounds__(THREADS) read_kv_kernel(KvView c, const int32_
 cudaError_t launch_append_kv(const KvView &c, const misa_new_kv &in, const int32_t *new_pos, int count,
                              const RopeView &r, const int32_t *rope_pos, bool commit, cudaStream_t s) {
   const int lpr = c.d / 16;
+  const bool after = commit && (overlap(new_pos, c.n_seq, c.seq_len, c.n_seq) ||
+                                (rope_pos && overlap(rope_pos, (int64_t)c.n_seq * count, c.seq_len, c.n_seq)));
   // without a rotation there is nothing to share between heads
   const int per = heads_per_thread((int64_t)c.n_seq * count * c.H_kv * lpr, r.phase ? c.H_kv : 1);
   const int head_groups = cdiv(c.H_kv, per);
@@ -223,20 +235,25 @@ cudaError_t launch_append_kv(const KvView &c, const misa_new_kv &in, const int32
   const int rot = !r.phase ? ROT_NONE : r.rot % 16 == 0 && r.first % 8 == 0 ? ROT_VEC : ROT_ANY;
   const dim3 g((unsigned)blocks, (unsigned)std::min(c.n_seq, 65535)), b(THREADS);
   auto go = [&](auto kernel) {
-    return launch_kernel(kernel, g, b, 0, s, c, in, new_pos, count, r, rope_pos, commit ? 1 : 0, head_groups);
+    return launch_kernel(kernel, g, b, 0, s, c, in, new_pos, count, r, rope_pos, commit && !after ? 1 : 0,
+                         head_groups);
   };
   auto by_rot = [&](auto none, auto vec, auto any) {
     return rot == ROT_NONE ? go(none) : rot == ROT_VEC ? go(vec) : go(any);
   };
+  cudaError_t e;
   if (c.d == 128)
-    return c.fp8 ? by_rot(append_kv_kernel<8, true, ROT_NONE>, append_kv_kernel<8, true, ROT_VEC>,
-                          append_kv_kernel<8, true, ROT_ANY>)
-                 : by_rot(append_kv_kernel<8, false, ROT_NONE>, append_kv_kernel<8, false, ROT_VEC>,
-                          append_kv_kernel<8, false, ROT_ANY>);
-  return c.fp8 ? by_rot(append_kv_kernel<4, true, ROT_NONE>, append_kv_kernel<4, true, ROT_VEC>,
-                        append_kv_kernel<4, true, ROT_ANY>)
-               : by_rot(append_kv_kernel<4, false, ROT_NONE>, append_kv_kernel<4, false, ROT_VEC>,
-                        append_kv_kernel<4, false, ROT_ANY>);
+    e = c.fp8 ? by_rot(append_kv_kernel<8, true, ROT_NONE>, append_kv_kernel<8, true, ROT_VEC>,
+                       append_kv_kernel<8, true, ROT_ANY>)
+              : by_rot(append_kv_kernel<8, false, ROT_NONE>, append_kv_kernel<8, false, ROT_VEC>,
+                       append_kv_kernel<8, false, ROT_ANY>);
+  else
+    e = c.fp8 ? by_rot(append_kv_kernel<4, true, ROT_NONE>, append_kv_kernel<4, true, ROT_VEC>,
+                       append_kv_kernel<4, true, ROT_ANY>)
+              : by_rot(append_kv_kernel<4, false, ROT_NONE>, append_kv_kernel<4, false, ROT_VEC>,
+                       append_kv_kernel<4, false, ROT_ANY>);
+  if (e != cudaSuccess || !after) return e;
+  return launch_kernel(commit_kv_kernel, dim3((unsigned)cdiv(c.n_seq, THREADS)), b, 0, s, c, new_pos, count);
 }
 
 cudaError_t launch_read_kv(const KvView &c, const int32_t *seq, const int32_t *tok, int n, int k, uint16_t *k_out,

@@ -37,7 +37,7 @@ def new(**f):
 
 
 def queries(**f):
-    return A.misa_attend_queries(**{**dict(q=FAKE, q_seq=FAKE, q_pos=FAKE, n_q=3, H=8, scale=0.1), **f})
+    return A.misa_attend_queries(**{**dict(q=FAKE << 8, q_seq=FAKE, q_pos=FAKE, n_q=3, H=8, scale=0.1), **f})
 
 
 def draft(**f):
@@ -108,20 +108,71 @@ def test_append_refusals():
         assert call(n=new(**{s: 132})) == INV
 
 
+def test_append_positions_that_overlap_the_lengths():
+    """seq_len itself may say where the tokens go; an array that shares a part of it may not."""
+    c = kv(n_seq=4)
+    for off in (-12, -4, 4, 12):
+        assert L.misa_append_kv(by(c), by(new()), c.seq_len + off, 1, None, None, 1, None) == INV
+    M.debug_fail_next(4)
+    try:
+        for off, commit in ((-4, 0), (0, 1), (16, 1), (-16, 1)):
+            assert L.misa_append_kv(by(c), by(new()), c.seq_len + off, 1, None, None, commit, None) == M.MISA_ERR_CUDA
+    finally:
+        M.debug_fail_next(0)
+
+
+def test_outputs_that_meet_are_refused():
+    c, q = kv(), queries()
+    size = q.n_q * q.H * c.d * 2
+    for off in (0, 16, size - 16, 16 - size):
+        assert L.misa_attend(by(c), by(q), FAKE, 4, None, q.q + off, None, FAKE, 1 << 30, None) == INV
+    rows_bytes = 3 * 4 * c.H_kv * c.d * 2
+    for off in (0, 16, rows_bytes - 16):
+        assert L.misa_read_kv(by(c), FAKE, FAKE, 3, 4, FAKE, FAKE + off, None) == INV
+    for bad in (dict(y_row=0, n=2), dict(y_head=0, H=2), dict(y_row=128, y_head=128, n=2, H=2),
+                dict(y_row=128, y_head=64, n=1, H=2, d=128), dict(y_row=256, y_head=256, n=2, H=2, d=128)):
+        bad = {"n": 2, "H": 2, "d": 128, **bad, "y": FAKE + (1 << 20)}
+        assert L.misa_apply_rope(by(rope()), by(rows(**bad)), 1, None) == INV, bad
+    two = (A.misa_rope_rows * 2)(rows(), rows())
+    assert L.misa_apply_rope(by(rope()), two, 2, None) == INV       # the same rows twice
+    two = (A.misa_rope_rows * 2)(rows(y=FAKE + (1 << 20)), rows(x=FAKE + (1 << 20), y=FAKE + (1 << 21)))
+    assert L.misa_apply_rope(by(rope()), two, 2, None) == INV       # what the other writes
+    M.debug_fail_next(3)
+    try:
+        good = dict(n=3, H=4, d=128, y=FAKE + (1 << 20))
+        for st in (dict(y_row=512, y_head=128), dict(y_row=128, y_head=384), dict(y_row=9000, y_head=2000)):
+            assert L.misa_apply_rope(by(rope()), by(rows(**good, **st)), 1, None) == M.MISA_ERR_CUDA
+    finally:
+        M.debug_fail_next(0)
+
+
+def test_host_tensors_are_refused():
+    """Pointers to host memory never reach a kernel."""
+    k = torch.zeros(1, 8, 1, 64, dtype=torch.bfloat16)
+    n = torch.zeros(1, dtype=torch.int32)
+    c = A.KVCache(k, k.clone(), None, None, n)
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    for call in (lambda: A.append_kv(c, k[:, :1], k[:, :1], n), lambda: A.read_kv(c, n, n.view(1, 1)),
+                 lambda: A.attend(c, A.AttentionQueries(x, n, n)),
+                 lambda: A.apply_rope(A.Rope(64, device="cpu"), [(x, n, x)])):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_read_refusals():
     c = kv()
-    assert L.misa_read_kv(by(c), FAKE, FAKE, -1, 1, FAKE, FAKE, None) == INV
-    assert L.misa_read_kv(by(c), FAKE, FAKE, 1, 0, FAKE, FAKE, None) == INV
-    assert L.misa_read_kv(by(c), None, FAKE, 1, 1, FAKE, FAKE, None) == INV
-    assert L.misa_read_kv(by(c), FAKE, None, 1, 1, FAKE, FAKE, None) == INV
+    assert L.misa_read_kv(by(c), FAKE, FAKE, -1, 1, FAKE, FAKE << 8, None) == INV
+    assert L.misa_read_kv(by(c), FAKE, FAKE, 1, 0, FAKE, FAKE << 8, None) == INV
+    assert L.misa_read_kv(by(c), None, FAKE, 1, 1, FAKE, FAKE << 8, None) == INV
+    assert L.misa_read_kv(by(c), FAKE, None, 1, 1, FAKE, FAKE << 8, None) == INV
     assert L.misa_read_kv(by(c), FAKE, FAKE, 1, 1, None, None, None) == INV
-    assert L.misa_read_kv(by(c), FAKE, FAKE, 1, 1, FAKE + 4, FAKE, None) == INV
+    assert L.misa_read_kv(by(c), FAKE, FAKE, 1, 1, FAKE + 4, FAKE << 8, None) == INV
 
 
 @pytest.mark.parametrize("bad,status", [(dict(q=None), INV), (dict(q_seq=None), INV), (dict(q_pos=None), INV),
                                         (dict(n_q=-1), INV), (dict(n_q=65536), INV), (dict(H=0), INV), (dict(H=6), INV),
                                         (dict(H=132), UNS), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV),
-                                        (dict(q=FAKE + 8), INV)])
+                                        (dict(q=(FAKE << 8) + 8), INV)])
 def test_attend_query_refusals(bad, status):
     assert L.misa_attend(by(kv()), by(queries(**bad)), FAKE, 4, None, FAKE, None, FAKE, 1 << 30, None) == status
 
@@ -158,7 +209,7 @@ def test_injected_failures():
         assert L.misa_append_kv(by(kv()), by(new()), FAKE, 0, None, None, 1, None) == INV  # consumes none
         assert L.misa_apply_rope(by(rope()), by(rows()), 1, None) == M.MISA_ERR_CUDA
         assert L.misa_append_kv(by(kv()), by(new()), FAKE, 1, None, None, 1, None) == M.MISA_ERR_CUDA
-        assert L.misa_read_kv(by(kv()), FAKE, FAKE, 1, 1, FAKE, FAKE, None) == M.MISA_ERR_CUDA
+        assert L.misa_read_kv(by(kv()), FAKE, FAKE, 1, 1, FAKE, FAKE << 8, None) == M.MISA_ERR_CUDA
         assert L.misa_attend(by(kv()), by(queries()), FAKE, 4, None, FAKE, None, FAKE, 1 << 30, None) == M.MISA_ERR_CUDA
         assert "injected" in M.last_error()
     finally:

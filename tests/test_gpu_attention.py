@@ -193,6 +193,40 @@ def test_append_rotated(layout, d, rot, first, e4m3):
     assert kv.seq_len.tolist() == [3 + count, kv.L_cap]
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_append_behind_what_is_there(e4m3):
+    """seq_len itself says where the tokens go, captured and replayed too."""
+    g, n_seq, count = gen(8), 300, 3
+    rope = A.Rope(32, device=DEV)
+    start = torch.randint(0, 20, (n_seq,), generator=g, device=DEV).int()
+    start[7], start[100] = -1, 38                      # stays; would pass the end
+    a, b = (A.KVCache.empty(n_seq, 40, 8, 128, e4m3) for _ in range(2))
+    a.seq_len.copy_(start), b.seq_len.copy_(start)
+    k, v = (randn(g, n_seq, count, 8, 128).bfloat16() for _ in range(2))
+    one = k[:, :1], v[:, :1]
+    pos = start.clone()
+
+    def plain(x, y, n):
+        A.append_kv(b, x, y, pos.clone(), rope=rope)
+        pos.copy_(torch.where((pos < 0) | (pos + n > 40), pos, pos + n))
+
+    A.append_kv(a, k, v, a.seq_len, rope=rope)
+    plain(k, v, count)
+    assert a.seq_len.tolist() == b.seq_len.tolist() == pos.tolist()
+    assert a.device_status() == b.device_status() == M.DEV_APPEND_RANGE
+    A.append_kv(a, *one, a.seq_len, rope=rope, rope_pos=a.seq_len)
+    plain(*one, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        A.append_kv(a, k, v, a.seq_len, rope=rope)
+    for _ in range(2):
+        graph.replay()
+        plain(k, v, count)
+    assert torch.equal(a.seq_len, b.seq_len)
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
+        assert x is None or torch.equal(x, y)
+
+
 def test_append_past_the_end_and_special_values():
     g = gen(6)
     kv = A.KVCache.empty(3, 16, 2, 64, True)
