@@ -24,6 +24,16 @@
 // memory, in a fixed order; more shares meet in the workspace, where
 // attend_combine_kernel joins them.
 //
+// Measured, heads of 128, e4m3.  Lists of 2048 tokens, 8 queries x 64 heads on
+// 8 key/value heads: 18.5 us, of which the stream of rows (35 MB) is about 8 and
+// the launch, the lists' look-up and the join of 8 shares the rest.  512
+// queries x 64 heads on 4: 196 us for 1.1 GB of gathered rows, and 128 x 64
+// on 8: 85 us for 0.56 GB; both are what the L2 gives to gathers of 128-byte
+// rows (5.5 to 6.6 TB/s): variants with more warps, with longer chunks and with
+// fewer instructions per chunk took the same time; issue slots are 41 % busy,
+// the tensor pipe 30 %.  Whole prefixes, 8 x 16K tokens, 4 heads per key/value
+// head: 62 us, 4.4 TB/s (bf16: 6.0 TB/s).
+//
 // Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
 // bf16 before they meet the values.  e4m3 caches: codes are exact in f16; a
 // tile's queries are scaled by a power of two into f16's range (bf16 has 8

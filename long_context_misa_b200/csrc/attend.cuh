@@ -226,9 +226,8 @@ __device__ __forceinline__ float2 ld_cluster2(const void *p, uint32_t rank) {
   return v;
 }
 
-// attend_umma.cu: the same attention for tiles of many rows (more than 32 heads
-// of a query, or of neighbouring queries of one sequence) on tcgen05 tensor
-// cores.  per: queries per tile; tiles: CTAs in x (each goes on by that many).
+// attend_umma.cu: the same attention for tiles of many rows (heads of a query,
+// or of neighbouring queries of one sequence) on tcgen05 tensor cores.  per: queries per tile; tiles: CTAs in x (each goes on by that many).
 cudaError_t launch_attend_umma(const KvView &c, const AttendView &a, const Split &sp, int per, int tiles,
                                cudaStream_t s);
 

@@ -1,7 +1,7 @@
 // Attention of tiles with many rows on tcgen05 tensor cores: more than 32
-// heads of a query, or of the neighbouring queries of one sequence (drafted
-// trees and prefill chunks over whole prefixes).  Same formulas, tokens and
-// numbers as attend.cu.
+// heads of a query with a list, more than 16 of the neighbouring queries of one
+// sequence (drafted trees and prefill chunks over whole prefixes).  Same
+// formulas, tokens and numbers as attend.cu.
 //
 // A CTA holds up to 128 rows (lanes of tensor memory) of one key/value head
 // and a share of the tokens, in chunks of 128:
@@ -21,8 +21,11 @@
 // A chunk (64 KB of bf16 rows) is 1024 cycles of MMA at M = 128 and 2850 of
 // the SM's share of HBM.  What decides is the MMA thread: an instruction costs
 // it 65 to 85 cycles, a commit or a wait 70, so S is issued at N = 128 for
-// both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences: 143 us
-// with chunks of 64).
+// both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences, 8
+// key/value heads: 101 us, 5.3 TB/s; 143 us with chunks of 64).  128 CTAs are
+// one wave there; a chunk takes 1.3 us, the beginning, the end and the join
+// about 15 us.  e4m3 rows have half the bytes but take 149 us: widening a chunk
+// costs its producer warps more than bringing it.
 #include <type_traits>
 
 #include "attend.cuh"

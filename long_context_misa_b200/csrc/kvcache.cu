@@ -10,6 +10,14 @@
 // of misa_append_keys_e4m3.  The key is rotated in fp32 first and not rounded
 // in between.  A thread keeps its 8 pairs' cos and sin for the heads of a
 // token that it takes one after the other.
+//
+// Measured, 8 key/value heads of 128.  Write of 2 x 8192 rotated tokens to e4m3
+// (102 MB): 28.7 us, 3.5 TB/s, issue slots 64 % busy: the codes are computed at
+// both ends of the quotient's interval, and about one warp in four goes through
+// the fp64 product.  Read of 8 x 2048 listed e4m3 tokens (102 MB with the
+// outputs): 20.6 us, 4.9 TB/s, issue slots 80 % busy with the conversions e4m3
+// -> f16 -> fp32 -> bf16.  A few rows: 4.1 us either way, the launch and its
+// dependent loads.
 #include <algorithm>
 
 #include "attention.h"
