@@ -12,12 +12,12 @@
 // token that it takes one after the other.
 //
 // Measured, 8 key/value heads of 128.  Write of 2 x 8192 rotated tokens to e4m3
-// (102 MB): 28.7 us, 3.5 TB/s, issue slots 64 % busy: the codes are computed at
-// both ends of the quotient's interval, and about one warp in four goes through
-// the fp64 product.  Read of 8 x 2048 listed e4m3 tokens (102 MB with the
-// outputs): 20.6 us, 4.9 TB/s, issue slots 80 % busy with the conversions e4m3
-// -> f16 -> fp32 -> bf16.  A few rows: 4.1 us either way, the launch and its
-// dependent loads.
+// (102 MB): 26.6 us, 3.8 TB/s (28.7 with codes taken at both ends of an interval
+// around the quotient and an fp64 product where they differed).  Read of 8 x 2048
+// listed e4m3 tokens (102 MB with the outputs): 20.7 us, 4.9 TB/s; forms with
+// fewer instructions (row numbers by multiplication, paired products) and with
+// two pieces per thread took 21.2 to 22.6.  A few rows: 4.1 us either way, the
+// launch and its dependent loads.
 #include <algorithm>
 
 #include "attention.h"
@@ -29,33 +29,63 @@ namespace {
 
 constexpr int THREADS = 128;
 
-// Four e4m3 codes of f[0..3] * by (nearest even, saturated), low byte first.
-__device__ __forceinline__ uint32_t codes4(const float *f, float by) {
-  uint32_t c;
-  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
-      : "=r"(c)
-      : "f"(f[0] * by), "f"(f[1] * by), "f"(f[2] * by), "f"(f[3] * by));
+// Two fp32 values in one register pair: sm_100's paired arithmetic.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Two e4m3 codes (nearest even, saturated), a's in the low byte.
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(a), "f"(b));
   return c;
 }
 
-// e4m3(f / sc) of 8 elements with the IEEE quotients.  f * inv (inv = 1 / sc to
-// an ulp) is within 2^-21 of the quotient, so where both ends of that interval
-// round to the same code the quotient is not needed.  Otherwise (ties are not
-// rare among bf16 inputs: about one warp in four meets one) the quotient comes
-// from a product in fp64: that is within 2^-52 of it, a quotient of two fp32
-// numbers that is not an fp32 number's midpoint lies at least 2^-49 away from
-// one, and an exact tie is an fp32 number itself, so rounding the product to
-// fp32 gives the IEEE quotient.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float sc, float inv) {
-  const float lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
-  const uint2 c = make_uint2(codes4(f, lo), codes4(f + 4, lo));
-  if (((c.x ^ codes4(f, hi)) | (c.y ^ codes4(f + 4, hi))) == 0u && inv <= 0x1p125f) return c;
-  const double r = 1.0 / (double)sc;
+// e4m3(f / sc) of 8 elements, f / sc rounded to fp32 in between.
+// near: y = 1 / sc rounded.  One correction of the product (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34, 1990): q0 = f y, q = q0 + y (f - sc q0).  q0 is within 2
+// ulp of f / sc, 1 - sc y within 2^-24, the remainder's rounding adds 2^-24 ulp:
+// before its last rounding q is within 3 * 2^-24 ulp of f / sc.  The code of q can
+// differ from that of the rounded quotient only where f / sc lies that close
+// to M + half an ulp or M - half an ulp, M a boundary between codes.  In half
+// ulps, with f = A 2^i, sc = B 2^j (A, B of 24 bits) and M = m 2^20 (m of 5
+// bits), that is |A 2^k - B (m 2^20 +- 1)| <= 6 * 2^-24 B < 6, k >= 24: a
+// nonzero B modulo 2^20 within 6 of 0.  near excludes such B; B = 0 modulo 2^20
+// leaves no number but 0 there, and 0 rounds alike.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float sc, float y, bool near) {
   float q[8];
+  if (near) {
+    // (-q is computed: that way around a -0 stays one)
+    const uint64_t yy = pair(-y, -y), ss = pair(sc, sc);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = (float)((double)f[i] * r);
-  return make_uint2(codes4(q, 1.f), codes4(q + 4, 1.f));
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t x = pair(f[i], f[i + 1]), q0 = mul2(x, yy);
+      const float2 t = unpair(fma2(fma2(ss, q0, x), yy, q0));
+      q[i] = -t.x, q[i + 1] = -t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(f[i], sc);
+  }
+  return make_uint2(codes2(q[0], q[1]) | codes2(q[2], q[3]) << 16, codes2(q[4], q[5]) | codes2(q[6], q[7]) << 16);
 }
 
 // 16 elements (chunks at o1 and o2 of a row) to the cache.  LPR threads hold
@@ -76,12 +106,16 @@ __device__ __forceinline__ void store_row(const float (&a)[8], const float (&b)[
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!store) return;
-  // m / 448 in IEEE rounding: m / 7 never lies within 2^-29 of an fp32 midpoint
-  // (relatively), far more than the fp64 product is off; denormal quotients
-  // take the division
-  const float sc = m >= 0x1p-100f ? (float)((double)m * (1.0 / 448.0)) : m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
-  const float inv = __fdividef(1.f, sc);
-  const uint2 x = codes8(a, sc, inv), y = codes8(b, sc, inv);
+  // m / 448, corrected once as in codes8: the divisor's significand is 7 * 2^21,
+  // so no quotient lies nearer to a midpoint than a seventh of half an ulp
+  constexpr float R448 = 1.f / 448.f;
+  const float s0 = m * R448;
+  const bool normal = m >= 0x1p-71f && m <= 0x1p120f;  // no remainder below fp32's range, nothing infinite
+  const float sc = normal ? fmaf(fmaf(-448.f, s0, m), R448, s0) : m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+  const uint32_t low = __float_as_uint(sc) & 0xFFFFFu;
+  const bool near = (normal || m == 0.f) && (low == 0u || (low > 7u && low < 0x100000u - 7u));
+  const float inv = __frcp_rn(sc);
+  const uint2 x = codes8(a, sc, inv, near), y = codes8(b, sc, inv, near);
   uint8_t *to = cache + row * (LPR * 16);
   if (o2 == o1 + 8 && (o1 & 15) == 0) {
     *reinterpret_cast<uint4 *>(to + o1) = make_uint4(x.x, x.y, y.x, y.y);

@@ -227,6 +227,39 @@ def test_append_behind_what_is_there(e4m3):
         assert x is None or torch.equal(x, y)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_codes_are_the_rounded_quotients(d):
+    """Codes and scales bit for bit: every bf16 significand as a row's largest and as its elements, ties, zeros of
+    both signs, tiny and huge rows, and scales next to numbers of few bits."""
+    n = 4096
+    k, v = (torch.empty(1, n, 2, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g = gen(9)
+    top = (1.0 + torch.arange(128, device=DEV) / 128).repeat(n * 2 // 128).view(1, n, 2)
+    for t, e in ((k, torch.randint(-120, 120, (1, n, 2), generator=g, device=DEV)),
+                 (v, torch.randint(-6, 7, (1, n, 2), generator=g, device=DEV))):
+        x = torch.randint(-128, 129, (1, n, 2, d), generator=g, device=DEV) / 128.0
+        x = x * 2.0 ** -torch.randint(0, 22, (1, n, 2, 1), generator=g, device=DEV).float()
+        x[..., 0] = 1.0
+        x[..., 1], x[..., 2] = 0.0, -0.0
+        t.copy_((x.double() * top[..., None].double() * 2.0 ** e[..., None].double()).bfloat16())
+    k[:, 5], v[:, 6] = 0.0, -0.0
+    kv = A.KVCache.empty(1, n, 2, d, True)
+    A.append_kv(kv, k, v, ints([0]))
+    # rotated: fp32 rows, by an amplitude that puts their scales within a few ulp of numbers of four bits
+    for x, codes, scale in ((k, kv.k, kv.k_scale), (v, kv.v, kv.v_scale)):
+        want, ws = plain_codes(x[0])
+        assert torch.equal(scale[0], ws.view(n, 2)) and torch.equal(codes[0], want)
+    k.copy_(torch.randint(-256, 257, (1, n, 2, d), generator=g, device=DEV) / 256.0 * 448)
+    k[..., 0] = 448.0
+    for ulps in range(-9, 10):
+        amp = float(torch.tensor(1.5) * (1 + ulps * 2.0 ** -23))
+        rope = A.Rope(d, amplitude=amp, phases=torch.zeros(d // 2, dtype=torch.int64), device=DEV)
+        A.append_kv(kv, k, v, ints([0]), rope=rope)
+        x = k[0].float() * torch.tensor(amp, device=DEV)
+        want, ws = plain_codes(x)
+        assert torch.equal(kv.k_scale[0], ws.view(n, 2)) and torch.equal(kv.k[0], want)
+
+
 def test_append_past_the_end_and_special_values():
     g = gen(6)
     kv = A.KVCache.empty(3, 16, 2, 64, True)
