@@ -22,10 +22,13 @@
 // the SM's share of HBM.  What decides is the MMA thread: an instruction costs
 // it 65 to 85 cycles, a commit or a wait 70, so S is issued at N = 128 for
 // both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences, 8
-// key/value heads: 101 us, 5.3 TB/s; 143 us with chunks of 64).  128 CTAs are
+// key/value heads: 99 us, 5.4 TB/s; 143 us with chunks of 64).  128 CTAs are
 // one wave there; a chunk takes 1.3 us, the beginning, the end and the join
-// about 15 us.  e4m3 rows have half the bytes but take 149 us: widening a chunk
-// costs its producer warps more than bringing it.
+// about 15 us.  e4m3 rows have half the bytes but take 145 us: a softmax thread
+// weighs its 64 tokens in 2200 cycles there (1300 for bf16), of which its
+// exponentials are 1000 (two warps on a scheduler's special-function unit), the
+// rest are the tokens' scales and latencies; the widening keeps up (eight
+// producer warps, at 96 registers, made it 160 us).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -579,39 +582,49 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
 
         uint32_t pk[HALF / 2];  // P as it goes back to tensor memory
         auto weigh = [&](auto mk, float &sum) -> float {
-          float top = 0.f, s4[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t v[W][32];
+          float top = 0.f;
+          uint64_t s2[2] = {0u, 0u};  // (pairs of fp32)
+          const uint64_t mul_2 = pair(mul, mul), ref_2 = pair(-y_ref, -y_ref);
+          uint32_t v[FP8 ? 1 : W][32];
+          if (!FP8) {
 #pragma unroll
-          for (int w = 0; w < W; ++w) umma::ld32(ts + w * 32, v[w]);
-          umma::ld_wait();
+            for (int w = 0; w < W; ++w) umma::ld32(ts + w * 32, v[FP8 ? 0 : w]);
+            umma::ld_wait();
+          }
 #pragma unroll
           for (int w = 0; w < W; ++w) {
+            if (FP8) {  // (the scales need the registers)
+              umma::ld32(ts + w * 32, v[0]);
+              umma::ld_wait();
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              float k4[4] = {1.f, 1.f, 1.f, 1.f}, v4[4] = {1.f, 1.f, 1.f, 1.f}, wt[4];
+              float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f), v4 = k4;
               if (FP8) {
-                const float4 x = *reinterpret_cast<const float4 *>(ks + w * 32 + i);
-                const float4 y = *reinterpret_cast<const float4 *>(vs + w * 32 + i);
-                k4[0] = x.x, k4[1] = x.y, k4[2] = x.z, k4[3] = x.w;
-                v4[0] = y.x, v4[1] = y.y, v4[2] = y.z, v4[3] = y.w;
+                k4 = *reinterpret_cast<const float4 *>(ks + w * 32 + i);
+                v4 = *reinterpret_cast<const float4 *>(vs + w * 32 + i);
               }
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float x = fmaf(__uint_as_float(v[w][i + u]), FP8 ? k4[u] * mul : mul, -y_ref);
-                const bool seen = !mk.value || ((see[w] >> (i + u)) & 1u);
-                if (mk.value && !seen) x = NEG_INF;
-                const float p = ex2(x);
-                s4[u] += p;
-                wt[u] = p;
-                if (FP8) wt[u] = seen ? p * v4[u] : 0.f;
-                top = fmaxf(top, wt[u]);
+              for (int u = 0; u < 4; u += 2) {
+                const uint64_t k2 = FP8 ? mul2(u ? pair(k4.z, k4.w) : pair(k4.x, k4.y), mul_2) : mul_2;
+                float2 x = unpair(fma2(pair(__uint_as_float(v[FP8 ? 0 : w][i + u]), __uint_as_float(v[FP8 ? 0 : w][i + u + 1])), k2, ref_2));
+                const bool seen0 = !mk.value || ((see[w] >> (i + u)) & 1u), seen1 = !mk.value || ((see[w] >> (i + u + 1)) & 1u);
+                if (mk.value) x.x = seen0 ? x.x : NEG_INF, x.y = seen1 ? x.y : NEG_INF;
+                const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                const uint64_t p2 = pair(p.x, p.y);
+                s2[u >> 1] = add2(s2[u >> 1], p2);
+                float2 wt = p;
+                if (FP8) {
+                  wt = unpair(mul2(p2, u ? pair(v4.z, v4.w) : pair(v4.x, v4.y)));
+                  if (mk.value) wt.x = seen0 ? wt.x : 0.f, wt.y = seen1 ? wt.y : 0.f;
+                }
+                top = fmaxf(top, fmaxf(wt.x, wt.y));
+                pk[(w * 32 + i + u) / 2] = FP8 ? f16x2(wt.x, wt.y) : bf16x2(wt.x, wt.y);
               }
-#pragma unroll
-              for (int u = 0; u < 4; u += 2)
-                pk[(w * 32 + i + u) / 2] = FP8 ? f16x2(wt[u], wt[u + 1]) : bf16x2(wt[u], wt[u + 1]);
             }
           }
-          sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          const float2 s0 = unpair(add2(s2[0], s2[1]));
+          sum = s0.x + s0.y;
           return FP8 && sum > SUM_MAX ? 2.f * LAZY : top;
         };
         float sum = 0.f, top = LAZY + 1.f;

@@ -29,28 +29,6 @@ namespace {
 
 constexpr int THREADS = 128;
 
-// Two fp32 values in one register pair: sm_100's paired arithmetic.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
-  return p;
-}
-__device__ __forceinline__ float2 unpair(uint64_t p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-  return f;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // Two e4m3 codes (nearest even, saturated), a's in the low byte.
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
   uint16_t c;
