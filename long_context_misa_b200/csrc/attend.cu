@@ -674,10 +674,10 @@ struct Plan {
 //
 // More than 16 rows without lists, or 32 with them, go to the tcgen05 kernel.
 // Measured on both (us, mma.sync / tcgen05; 8 sequences, 8 key/value heads of
-// 128): 12 rows over 16K bf16 tokens 89 / 98 and e4m3 74 / 170, 24 rows 152 /
-// 100 and 249 / 172; 12 rows over 1000 tokens 21 / 25 and 21 / 35, 24 rows
-// 29 / 27 and 33 / 36; lists of 2048 tokens (2 key/value heads), 16 rows 12 /
-// 16 and 12 / 21, 32 rows 16 / 16 and 18 / 21.
+// 128): 12 rows over 16K bf16 tokens 89 / 92 and e4m3 74 / 137, 24 rows 152 / 93
+// and 249 / 137; 12 rows over 1000 tokens 20 / 20 and 21 / 28, 24 rows 29 / 21 and
+// 33 / 29; lists of 2048 tokens (2 key/value heads), 16 rows 10 / 15 and 11 / 21,
+// 32 rows 14 / 16 and 19 / 21.
 Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   Plan p;
   const int G = H / c.H_kv;

@@ -22,7 +22,7 @@
 // the SM's share of HBM.  What decides is the MMA thread: an instruction costs
 // it 65 to 85 cycles, a commit or a wait 70, so S is issued at N = 128 for
 // both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences, 8
-// key/value heads: 99 us, 5.4 TB/s; 143 us with chunks of 64).  128 CTAs are
+// key/value heads: 98 us, 5.5 TB/s; 143 us with chunks of 64).  128 CTAs are
 // one wave there; a chunk takes 1.3 us, the beginning, the end and the join
 // about 15 us.  e4m3 rows have half the bytes but take 145 us: a softmax thread
 // weighs its 64 tokens in 2200 cycles there (1300 for bf16), of which its
