@@ -369,8 +369,8 @@ def attend_workspace_bytes(kv: KVCache, qs: AttentionQueries, k: int = 0, n_draf
 def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = None, draft: Optional[Draft] = None,
            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None,
            with_lse: bool = False, stream=None):
-    """Attention over the tokens of topk [n_q][k] (-1 padded, as the top-k calls write it), or over whole prefixes
-    (topk None), and the drafted slots that each query's mask shows.
+    """Attention over the tokens of topk [n_q][k] (-1 padded, as the top-k calls write it; k may be 0: no tokens), or
+    over whole prefixes (topk None), and the drafted slots that each query's mask shows.
 
     Returns out [n_q][H][d] (q's type), with ``with_lse`` or a given ``lse`` the pair (out, lse fp32 [n_q][H])."""
     dev = kv.device
@@ -402,6 +402,11 @@ def attend(kv: KVCache, qs: AttentionQueries, topk: Optional[torch.Tensor] = Non
         if lse.shape != (qs.n_q, qs.H) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{qs.n_q}][{qs.H}], got {tuple(lse.shape)}")
         _on(lse, dev, "lse")
+    if topk is not None and k == 0:
+        # a list of nothing: one entry of nothing per query (without a list the whole prefix would be seen)
+        k = 1
+        with _allocating(stream):
+            topk = torch.full((qs.n_q, 1), -1, dtype=torch.int32, device=dev)
     key = (k, n_draft, kv._shape)
     need = qs._need.get(key)
     if need is None:

@@ -341,3 +341,22 @@ def test_binding_refusals():
         A.apply_rope(r, [(x, idx, x[:2])])
     with pytest.raises(ValueError):
         A.apply_rope(r, [(x.transpose(1, 2), idx, x.transpose(1, 2))])
+
+
+def test_a_list_of_nothing_stays_a_list(monkeypatch):
+    """topk [n_q][0] has no memory (a NULL pointer): the call must not take it for the absence of a list."""
+    k = torch.zeros(2, 16, 4, 128, dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    c = A.KVCache(k, k.clone(), None, None, n)
+    seen = []
+
+    def call(fn, device, stream, kv_p, qs_p, topk, entries, *rest):
+        seen.append((entries, (ctypes.c_int32 * (3 * entries)).from_address(topk)[:]))
+
+    monkeypatch.setattr(A, "_call", call)
+    idx = torch.zeros(3, dtype=torch.int32)
+    qs = A.AttentionQueries(torch.zeros(3, 8, 128, dtype=torch.bfloat16), idx, idx)
+    for topk in (torch.empty(3, 0, dtype=torch.int32), torch.zeros(3, 5, dtype=torch.int32)[:, :0]):
+        A.attend(c, qs, topk=topk)
+        A.attend(c, qs, topk=topk, draft=A.Draft(n, torch.zeros(3, 1, dtype=torch.int32), 3))
+    assert seen == [(1, [-1, -1, -1])] * 4

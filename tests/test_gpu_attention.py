@@ -519,6 +519,20 @@ def test_empty_sequence_and_empty_batch(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("G", [3, 40])
+def test_lists_without_entries(e4m3, G):
+    """A list of nothing shows the drafted tokens alone; without them nothing."""
+    c = Case(e4m3, 128, 2, G, lens=(50, 20), per=(2, 2), drafts=3, seed=46)
+    c.topk = torch.empty(4, 0, dtype=torch.int32, device=DEV)
+    c.poison()
+    c.run()
+    c.draft = None
+    out, lse = c.run()
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
 def test_lists_in_any_order_with_repeats_and_strangers(e4m3):
     c = Case(e4m3, 128, 2, 4, lens=(300, 200), per=(1, 2), k=64, seed=34)
     g = c.g
