@@ -713,7 +713,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             }
             if (!(ok = meet())) break;
             const int found = sh.n_bad[g];
-            if (found == 0) break;
+            // the count is read by all before the next scan adds to it: S is a
+            // chunk ahead, so a warp may be there while another still reads
+            if (found == 0) {
+              ok = meet();
+              break;
+            }
             if (j > 0 && !(ok = wait(&sh.pvdone[g], (j - 1) & 1))) break;  // O may change now
             umma::fence_after();
             for (int i = 0; i < min(found, BAD); ++i) {
