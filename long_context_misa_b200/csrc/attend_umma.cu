@@ -100,6 +100,13 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   return true;
 }
 
+// The same by a whole warp: true in every lane or in none.  A phase may complete
+// between two lanes' last polls, and lanes that went on alone would wait for
+// ever at the warp's next ballot, vote or tensor-memory access.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, const KvView &c) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, c)) != 0;
+}
+
 // MN-major, 128-byte swizzle: atoms of 64 elements x 8 k-rows of 128 B; LBO
 // steps between 64-element blocks, SBO between groups of 8 k-rows.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block_bytes) {
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           if (notes) sh.have[j & (SLOTS - 1)][(pt >> 5) + 2 * h] = b;
         }
         mbar_arrive(&sh.placed[vals]);
-        return wait_bar(&sh.placed[vals], meetings++ & 1, abort, c);
+        return wait_warp(&sh.placed[vals], meetings++ & 1, abort, c);
       };
       const int pc = pt % CPR, r0 = pt / CPR;
       constexpr int RSTEP = GROUP / CPR;
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       };
       if (!FP8) {
         for (int j = 0; j < n; ++j) {
-          if (j >= nst && !wait_bar(&empty[st], wrap, abort, c)) break;
+          if (j >= nst && !wait_warp(&empty[st], wrap, abort, c)) break;
           if (!place(j)) break;
           const uint32_t dst = smem_addr(ring + st * TILE);
           if (by_tma(j)) {
@@ -410,8 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             if (!place(j)) return false;
             const uint32_t dst = smem_addr(raw + (j % NR) * F::RAW);
             if (by_tma(j)) {
+              // (only pt 0 refills the tile, but its warp goes on or leaves as one)
+              if (pt < 32 && j >= NR && !wait_warp(&sh.rawempty[vals][j % NR], ((j / NR) & 1) ^ 1, abort, c)) return false;
               if (pt == 0) {
-                if (j >= NR && !wait_bar(&sh.rawempty[vals][j % NR], ((j / NR) & 1) ^ 1, abort, c)) return false;
                 mbar_arrive_expect_tx(&sh.rawfull[vals][j % NR], F::RAW);
                 umma::tma_load_3d(dst, map, 0, hk, seq * c.L_cap + (cb + j) * TOK, &sh.rawfull[vals][j % NR]);
               }
@@ -430,8 +438,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         for (int j = 0; j < n && ok; ++j) {
           if (!(ok = bring(j + NR - 1))) break;
           cp_async_wait<NR - 1>();
-          if (by_tma(j) && !(ok = wait_bar(&sh.rawfull[vals][j % NR], (j / NR) & 1, abort, c))) break;
-          if (j >= nst && !(ok = wait_bar(&empty[st], wrap, abort, c))) break;
+          if (by_tma(j) && !(ok = wait_warp(&sh.rawfull[vals][j % NR], (j / NR) & 1, abort, c))) break;
+          if (j >= nst && !(ok = wait_warp(&empty[st], wrap, abort, c))) break;
           const uint8_t *from = raw + (j % NR) * F::RAW + pt * 16;
           uint8_t *dst = ring + st * TILE;
 #pragma unroll 8
@@ -533,8 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       };
 #pragma unroll
       for (int w = 0; w < W; ++w) drafted[w] = draft_word(g * HALF + w * 32);
-      // bounded waits of a whole warp (its tensor-memory accesses need all lanes)
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, c)) != 0; };
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort, c); };
       auto meet = [&]() {  // the 128 threads of the set
         mbar_arrive(&sh.scan[g]);
         return wait(&sh.scan[g], scans++ & 1);

@@ -7,6 +7,10 @@
   routes while the append kernel before it still runs (that append triggers
   it early), reading only what the append does not write; it starts with
   grid_dep_sync_unless(...) and waits before anything else.
+- In the tcgen05 attention kernel a wait that can run out leaves a warp whole:
+  softmax and producer warps vote on it (wait_warp), because their later
+  ballots and tensor-memory accesses wait for every lane without a limit.  Only
+  the MMA issuer, one thread without warp-wide operations, waits by itself.
 - Every launch goes through launch_kernel (the one place that sets the launch
   attributes); no triple-chevron launches.
 """
@@ -65,6 +69,19 @@ def test_only_the_append_triggers_early():
         if "grid_dep_launch()" in src and not p.endswith("common.cuh"):
             users.append(os.path.basename(p))
     assert users == ["pool.cu"], users
+
+
+def test_warps_leave_bounded_waits_whole():
+    src = _strip_comments(open(os.path.join(CSRC, "attend_umma.cu")).read())
+    voted = re.search(r"bool wait_warp\([^)]*\) \{\s*return __all_sync\(0xffffffffu, wait_bar\([^)]*\)\) != 0;\s*\}", src)
+    assert voted
+    issuer = src[src.index("} else if (warp == MMA_WARP) {"):]
+    issuer = issuer[:issuer.index("} else {\n", issuer.index("mbar_wait(&sh.done, 0)"))]
+    assert "if (lane == 0" in issuer and "_sync(0xffffffff" not in issuer
+    definition = re.search(r"bool wait_bar\(", src).group(0)
+    rest = src.replace(voted.group(0), "").replace(issuer, "").replace(definition, "", 1)
+    assert "wait_bar(" not in rest and "mbar_wait(" not in rest and "try_wait" not in rest.split("WAIT_LIMIT_NS", 1)[1]
+    assert rest.count("wait_warp(") >= 6
 
 
 def test_kernel_count():
