@@ -243,8 +243,9 @@ typedef struct {
  * Numbers: products of the stored values with fp32 sums; softmax statistics
  * in fp32.  bf16 caches: the weights exp(s_t - ref), ref a running maximum of
  * s_t, are rounded to bf16 before they meet the values.  e4m3 caches: the
- * codes are exact in f16; q is scaled by one power of two per group of rows
- * and exp(s_t - ref) v_scale_t, ref a running maximum of s_t + ln v_scale_t
+ * codes are exact in f16; each row of q is scaled by a power of two of its own
+ * (elements down to 2^-23 of the row's largest stay exact) and
+ * exp(s_t - ref) v_scale_t, ref a running maximum of s_t + ln v_scale_t
  * (v_scale_t held within 2^-100 and 2^100 there), is rounded to f16.
  * Workspace: misa_attend_workspace_bytes(kv, qs, k, draft ? draft->n : 0),
  * 16-byte aligned.  Results do not depend on what it held.

@@ -35,9 +35,9 @@
 // head: 62 us, 4.4 TB/s (bf16: 6.0 TB/s).
 //
 // Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
-// bf16 before they meet the values.  e4m3 caches: codes are exact in f16; a
-// tile's queries are scaled by a power of two into f16's range (bf16 has 8
-// significant bits, so elements down to 2^-24 of the tile's largest stay
+// bf16 before they meet the values.  e4m3 caches: codes are exact in f16; each
+// row of queries is scaled by a power of two of its own into f16's range (bf16
+// has 8 significant bits, so elements down to 2^-23 of the row's largest stay
 // exact).  With ref the running maximum of s_t + ln v_scale_t, the sum of the
 // weights e^(s_t - ref) stays in fp32, and what meets the value codes is
 // e^(s_t - ref) v_scale_t in f16: a row's largest contribution, not its
@@ -201,7 +201,6 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
     // ---- query fragments, the k dimension permuted so that a lane's 16-byte
     // pieces of a key row feed whole A fragments ----
     uint2 qf[Q_SMEM ? 1 : KT][Q_SMEM ? 1 : NR];
-    float sc = 1.f;
     auto row_piece = [&](int n, int i) {
       const int r = n * 8 + g;
       // e4m3: 16 elements at 64 ch + 16 c4 (pieces 2 ch, 2 ch + 1 of the lane);
@@ -210,25 +209,31 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       return r < n_rows ? *reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH + d0)
                         : make_uint4(0u, 0u, 0u, 0u);
     };
-    if (FP8) {
+    // of a product, to a base-2 logit: of this lane's columns, and (e4m3) the
+    // power of two of the row that it loads
+    float mul[NR][2], sc[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      sc[n] = 1.f;
+      mul[n][0] = mul[n][1] = a.scale * LOG2E;
+      if (!FP8) continue;
       float m = 0.f;
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+      for (int i = 0; i < DH / 32; ++i) {
+        const uint4 v = row_piece(n, i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-          const uint4 v = row_piece(n, i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const float2 f = bf16x2_to_float2(w[p]);
-            m = finite_max(finite_max(m, f.x), f.y);
-          }
+        for (int p = 0; p < 4; ++p) {
+          const float2 f = bf16x2_to_float2(w[p]);
+          m = finite_max(finite_max(m, f.x), f.y);
         }
+      }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the row's four lanes
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      sc[n] = f16_scale(m);
 #pragma unroll
-      for (int b = 1; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
-      sc = f16_scale(m);
+      for (int x = 0; x < 2; ++x) mul[n][x] *= __shfl_sync(0xffffffffu, inverse(sc[n]), (2 * c4 + x) * 4);
     }
-    const float mul = a.scale * LOG2E / sc;  // of a product, to a base-2 logit
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       if (Q_SMEM && n != warp % NR) continue;  // a warp's share (warps beyond NR repeat, harmlessly)
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const float2 f = bf16x2_to_float2(w[p]);
-            w[p] = f16x2(f.x * sc, f.y * sc);
+            w[p] = f16x2(f.x * sc[n], f.y * sc[n]);
           }
         }
 #pragma unroll
@@ -434,10 +439,10 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
 
       // ---- weights of the tokens g + 8 y for the columns x: p = e^(s - ref)
       // for the sum, w for the values ----
-      float km[2 * MTL], vs[2 * MTL];
+      float ks[2 * MTL], vs[2 * MTL];
 #pragma unroll
       for (int y = 0; y < 2 * MTL; ++y) {
-        km[y] = FP8 ? ss[g + 8 * y] * mul : mul;
+        ks[y] = FP8 ? ss[g + 8 * y] : 1.f;
         vs[y] = FP8 ? ss[CH + g + 8 * y] : 1.f;
       }
       float p[NR][4 * MTL], w[NR][4 * MTL], l_new[NR][2];
@@ -447,14 +452,19 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       auto weigh = [&](auto m) -> bool {  // m: std::true_type where something is masked
         float top = 0.f;
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NR; ++n) {
+          l_new[n][0] = l_new[n][1] = 0.f;
+          const uint64_t mul_2 = pair(mul[n][0], mul[n][1]), ref_2 = pair(-y_ref[n][0], -y_ref[n][1]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            l_new[n][x] = 0.f;
+          for (int y = 0; y < 2 * MTL; ++y) {
+            const float s0 = s[n][y >> 1][2 * (y & 1)], s1 = s[n][y >> 1][2 * (y & 1) + 1];
+            // (a row's factor last: its power of two and the token's scale may pass fp32's range between them)
+            const float2 v2 = FP8 ? unpair(fma2(mul2(pair(s0, s1), pair(ks[y], ks[y])), mul_2, ref_2))
+                                  : make_float2(fmaf(s0, mul[n][0], -y_ref[n][0]), fmaf(s1, mul[n][1], -y_ref[n][1]));
 #pragma unroll
-            for (int y = 0; y < 2 * MTL; ++y) {
+            for (int x = 0; x < 2; ++x) {
               const int e = 2 * y + x;
-              const float v = logit(m, fmaf(s[n][y >> 1][e & 3], km[y], -y_ref[n][x]), n, x, y);
+              const float v = logit(m, x ? v2.y : v2.x, n, x, y);
               p[n][e] = ex2(v);
               w[n][e] = FP8 ? p[n][e] * vs[y] : p[n][e];
               // (rows gathered for others may hold any scale)
@@ -462,8 +472,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
               l_new[n][x] += p[n][e];
               top = fmaxf(top, w[n][e]);
             }
-            if (FP8 && l_new[n][x] > SUM_MAX) top = 2.f * LAZY;
           }
+          if (FP8 && fmaxf(l_new[n][0], l_new[n][1]) > SUM_MAX) top = 2.f * LAZY;
+        }
         return __any_sync(0xffffffffu, top > LAZY);
       };
       for (bool again = false;; again = true) {
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
             float my = NEG_INF;
 #pragma unroll
             for (int y = 0; y < 2 * MTL; ++y)
-              my = fmaxf(my, logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * km[y], n, x, y) +
+              my = fmaxf(my, logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * ks[y] * mul[n][x], n, x, y) +
                                  (FP8 ? log2_scale(vs[y]) : 0.f));
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));

@@ -46,8 +46,10 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 __device__ __forceinline__ float f16_scale(float amax) {
   if (!(amax > 0.f)) return 1.f;
   const int e = 7 - ((int)(__float_as_uint(amax) >> 23) - 126);
-  return ldexpf(1.f, min(max(e, -126), 126));
+  return __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23);
 }
+// 1 / s of such a power of two, by its exponent
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 
 // max(m, |x|), where x is finite
 __device__ __forceinline__ float finite_max(float m, float x) {

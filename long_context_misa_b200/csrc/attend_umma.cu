@@ -75,7 +75,8 @@ struct Shared {
   int row_idx[2][2][TOK];   // [keys / values][turn][row of the chunk]: row in the sequence, -1 none
   uint32_t have[SLOTS][2 * W];  // which tokens of a chunk are there
   int len[M], query[M];
-  int seq, max_len, min_len, q_max;
+  float mul[M];  // of a row's products, to base-2 logits
+  int seq, max_len, min_len;
   int n_bad[2];
   int2 bad_at[2][BAD];  // (token, element)
   float bad_val[2][BAD];
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         mbar_init(&sh.pvdone[i], 1), mbar_init(&sh.placed[i], GROUP), mbar_init(&sh.scan[i], 128);
       mbar_init(&sh.done, 1), mbar_init(&sh.joined, 256);
       fence_mbar_init();
-      sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff, sh.q_max = 0;
+      sh.seq = -1, sh.max_len = 0, sh.min_len = 0x7fffffff;
       sh.n_bad[0] = sh.n_bad[1] = 0;
     }
     __syncthreads();
@@ -229,40 +230,34 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       sh.query[r] = r < n_rows ? row_query(r) : -1;
     }
     // ---- Q: 16-bit rows, K-major with 128-byte swizzle; e4m3 caches: f16
-    // after a power of two ----
+    // after a power of two of each row ----
     constexpr int QL = DH / 8, QT = THREADS - M;  // pieces of a row; threads (the others look up the rows meanwhile)
     auto q_piece = [&](int r, int p) {
       return r < n_rows ? reinterpret_cast<const uint4 *>(a.q + ((int64_t)row_query(r) * a.H + row_head(r)) * DH)[p]
                         : make_uint4(0u, 0u, 0u, 0u);
     };
-    float sc = 1.f;
-    if (FP8) {
-      float m = 0.f;
-      for (int e = tid - M; tid >= M && e < n_rows * QL; e += QT) {
-        const uint4 v = q_piece(e / QL, e % QL);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = bf16x2_to_float2(w[i]);
-          m = finite_max(finite_max(m, f.x), f.y);
-        }
-      }
-      atomicMax(&sh.q_max, __float_as_int(m));  // (positive floats order as integers)
-      __syncthreads();
-      sc = f16_scale(__int_as_float(sh.q_max));
-    }
-    const float mul = a.scale * LOG2E / sc;  // of a product, to a base-2 logit
+    // (M * QL and QT are whole warps, and the QL lanes of a row are of one)
     for (int e = tid - M; tid >= M && e < M * QL; e += QT) {
       const int r = e / QL, p = e % QL;
       uint4 v = q_piece(r, p);
       if (FP8) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(w[i]);
+          m = finite_max(finite_max(m, f.x), f.y);
+        }
+#pragma unroll
+        for (int b = 1; b < QL; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+        const float sc = f16_scale(m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = bf16x2_to_float2(w[i]);
           w[i] = f16x2(f.x * sc, f.y * sc);
         }
         v = make_uint4(w[0], w[1], w[2], w[3]);
+        if (p == 0) sh.mul[r] = a.scale * LOG2E * inverse(sc);
       }
       *reinterpret_cast<uint4 *>(q_s + tile_at(r, p, F::QBLK)) = v;
     }
@@ -527,6 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
       const int g = warp >> 2, r = tid & 127;
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = tl + T_O + g * 128;
       const int my_len = sh.len[r], my_query = sh.query[r];
+      const float mul = FP8 ? sh.mul[r] : a.scale * LOG2E;
       float y_ref = NOTHING, l_sum = 0.f;  // base-2 reference of O and of the sum, and the sum
       bool ok = true;
       int scans = 0;
@@ -613,8 +609,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               }
 #pragma unroll
               for (int u = 0; u < 4; u += 2) {
-                const uint64_t k2 = FP8 ? mul2(u ? pair(k4.z, k4.w) : pair(k4.x, k4.y), mul_2) : mul_2;
-                float2 x = unpair(fma2(pair(__uint_as_float(v[FP8 ? 0 : w][i + u]), __uint_as_float(v[FP8 ? 0 : w][i + u + 1])), k2, ref_2));
+                uint64_t x2 = pair(__uint_as_float(v[FP8 ? 0 : w][i + u]), __uint_as_float(v[FP8 ? 0 : w][i + u + 1]));
+                // (the row's factor last: its power of two and a token's scale may pass fp32's range between them)
+                if (FP8) x2 = mul2(x2, u ? pair(k4.z, k4.w) : pair(k4.x, k4.y));
+                float2 x = unpair(fma2(x2, mul_2, ref_2));
                 const bool seen0 = !mk.value || ((see[w] >> (i + u)) & 1u), seen1 = !mk.value || ((see[w] >> (i + u + 1)) & 1u);
                 if (mk.value) x.x = seen0 ? x.x : NEG_INF, x.y = seen1 ? x.y : NEG_INF;
                 const float2 p = make_float2(ex2(x.x), ex2(x.y));
@@ -646,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             const uint32_t sw = w == 0 ? see[0] : see[1];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] * mul : mul);
+              const float x = __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] : 1.f) * mul;
               if ((sw >> i) & 1u) my = fmaxf(my, FP8 ? x + log2_scale(vs[w * 32 + i]) : x);
             }
           }

@@ -723,6 +723,27 @@ def test_queries_of_any_magnitude(G, k):
     assert torch.equal(out[1, 2], want[1, 2]) and not bool(torch.isfinite(out[1, 1].float()).all())
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("G", [3, 8, 12, 20, 40])
+@pytest.mark.parametrize("k", [0, 64])
+def test_rows_of_very_different_magnitude(e4m3, G, k):
+    """Heads and queries side by side whose q differ by more than f16's range, and rows that see nothing whatever they
+    hold: no row costs another any bits."""
+    c = Case(e4m3, 128, 2, G, lens=(150, 90), per=(4, 3), k=k, seed=48)
+    c.q[0] *= 2.0 ** -60
+    c.q[0] *= 2.0 ** -40                               # a query at 2^-100
+    c.q[1, 1::3] *= 2.0 ** 12                          # heads of one query, 2^32 apart
+    c.q[1, 2::3] *= 2.0 ** -20
+    c.q[2] = 0
+    c.pos[5] = -1                                      # padding: sees nothing
+    c.q[5] = 3e38
+    if k:
+        c.topk[5] = -1
+    out, lse = c.run()
+    assert not bool(out[5].any()) and bool((lse[5] == -math.inf).all())
+    assert c.kv.device_status() == 0
+
+
 @pytest.mark.parametrize("G", [4, 24])
 def test_scales_of_very_different_size(G):
     """e4m3 rows whose scales span many orders, zero among them."""
