@@ -245,8 +245,9 @@ typedef struct {
  * s_t, are rounded to bf16 before they meet the values.  e4m3 caches: the
  * codes are exact in f16; each row of q is scaled by a power of two of its own
  * (elements down to 2^-23 of the row's largest stay exact) and
- * exp(s_t - ref) v_scale_t, ref a running maximum of s_t + ln v_scale_t
- * (v_scale_t held within 2^-100 and 2^100 there), is rounded to f16.
+ * exp(s_t - ref) v_scale_t, ref 7 ln 2 below a running maximum of
+ * s_t + ln v_scale_t (v_scale_t held within 2^-93 and 2^100 there), is rounded to
+ * f16: contributions below 2^-21 of a row's largest are off by up to 2^-32 of it.
  * Workspace: misa_attend_workspace_bytes(kv, qs, k, draft ? draft->n : 0),
  * 16-byte aligned.  Results do not depend on what it held.
  * Errors: those of the cache; MISA_ERR_INVALID for NULL q/q_seq/q_pos/out,

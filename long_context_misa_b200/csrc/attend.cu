@@ -17,8 +17,8 @@
 // m16n8k16 (S^T = K Q^T, O^T += V^T P^T), the rows the N side: 8 rows pad
 // nothing where M would pad to 16, and a lane keeps two tokens' scales.  P^T
 // turns from accumulator to operand by movmatrix.  The maximum is lazy: while
-// no logit exceeds the reference by 2^8 (base 2) nothing is rescaled and no
-// lane exchanges anything.
+// no weight grows by more than 2^8 nothing is rescaled and no lane exchanges
+// anything.
 // The warps' (max, sum, O) meet in shared memory at the end.  Up to 8 shares
 // are the CTAs of a thread-block cluster and join over its distributed shared
 // memory, in a fixed order; more shares meet in the workspace, where
@@ -38,10 +38,11 @@
 // bf16 before they meet the values.  e4m3 caches: codes are exact in f16; each
 // row of queries is scaled by a power of two of its own into f16's range (bf16
 // has 8 significant bits, so elements down to 2^-23 of the row's largest stay
-// exact).  With ref the running maximum of s_t + ln v_scale_t, the sum of the
-// weights e^(s_t - ref) stays in fp32, and what meets the value codes is
-// e^(s_t - ref) v_scale_t in f16: a row's largest contribution, not its
-// largest scale, sets f16's range.
+// exact).  With ref 7 binary orders below the running maximum of
+// s_t + ln v_scale_t, the sum of the weights e^(s_t - ref) stays in fp32, and
+// what meets the value codes is e^(s_t - ref) v_scale_t in f16: a row's largest
+// contribution, not its largest scale, sets f16's range, and what it loses is
+// 2^-32 of that.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -473,9 +474,9 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
               top = fmaxf(top, w[n][e]);
             }
           }
-          if (FP8 && fmaxf(l_new[n][0], l_new[n][1]) > SUM_MAX) top = 2.f * LAZY;
+          if (FP8 && fmaxf(l_new[n][0], l_new[n][1]) > SUM_MAX) top = 2.f * LAZY<FP8>;
         }
-        return __any_sync(0xffffffffu, top > LAZY);
+        return __any_sync(0xffffffffu, top > LAZY<FP8>);
       };
       for (bool again = false;; again = true) {
         const bool above = masked ? weigh(std::true_type()) : weigh(std::false_type());
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
                                  (FP8 ? log2_scale(vs[y]) : 0.f));
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));
-            const float y_new = fmaxf(y_ref[n][x], my);
+            const float y_new = fmaxf(y_ref[n][x], my - BELOW<FP8>);
             const float al = ex2(y_ref[n][x] - y_new);
             l_sum[n][x] *= al;
 #pragma unroll

@@ -6,7 +6,15 @@
 
 namespace misa {
 
-constexpr float LAZY = 256.f;  // most that a weight may reach before its reference moves
+// Binary orders between a row's largest weight and its reference when that
+// moves, and most that a weight may reach before it does.  e4m3 caches: f16
+// holds weights from 2^-25 to 2^16, so the largest starts at 2^7 and what is
+// lost lies 2^-32 below it (2^18 tokens of it: 2^-14); 2^8 times as much may
+// come without a move, as with bf16, whose range is fp32's.
+template <bool FP8>
+constexpr float BELOW = FP8 ? 7.f : 0.f;
+template <bool FP8>
+constexpr float LAZY = FP8 ? 0x1p15f : 256.f;
 // most that a chunk's weights may add to a row's sum before the reference moves:
 // rows of scale 0 add nothing to O, whatever they weigh (2^18 tokens of such
 // chunks still fit fp32)
@@ -57,10 +65,10 @@ __device__ __forceinline__ float finite_max(float m, float x) {
   return y < __int_as_float(0x7f800000) ? fmaxf(m, y) : m;
 }
 
-// log2 of a value scale for the reference of O, held within [-100, 100]: a row
+// log2 of a value scale for the reference of O, held within [-93, 100]: a row
 // of zeros (scale 0) or one that held an infinity must not move the others'
 // reference out of fp32's range.
-__device__ __forceinline__ float log2_scale(float s) { return __log2f(fminf(fmaxf(s, 0x1p-100f), 0x1p100f)); }
+__device__ __forceinline__ float log2_scale(float s) { return __log2f(fminf(fmaxf(s, 0x1p-93f), 0x1p100f)); }
 
 // Prefix length of query i (0 for none) and its sequence (-1: outside the
 // cache, it sees nothing).

@@ -16,7 +16,7 @@
 //                      tokens, with its own O and running maximum, so that
 //                      neither waits for the other; they join at the end.
 //                      Weights go back into the columns of S; O is touched
-//                      only when a weight passes 256 times its reference.
+//                      only when a weight has grown more than 256-fold.
 // Tensor memory: two O of 128 columns, two S (then P) of 128.
 // A chunk (64 KB of bf16 rows) is 1024 cycles of MMA at M = 128 and 2850 of
 // the SM's share of HBM.  What decides is the MMA thread: an instruction costs
@@ -630,11 +630,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           }
           const float2 s0 = unpair(add2(s2[0], s2[1]));
           sum = s0.x + s0.y;
-          return FP8 && sum > SUM_MAX ? 2.f * LAZY : top;
+          return FP8 && sum > SUM_MAX ? 2.f * LAZY<FP8> : top;
         };
-        float sum = 0.f, top = LAZY + 1.f;
+        float sum = 0.f, top = 2.f * LAZY<FP8>;
         if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
-        if (__any_sync(0xffffffffu, top > LAZY)) {
+        if (__any_sync(0xffffffffu, top > LAZY<FP8>)) {
           float my = NEG_INF;
 #pragma unroll 1
           for (int w = 0; w < W; ++w) {
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
               if ((sw >> i) & 1u) my = fmaxf(my, FP8 ? x + log2_scale(vs[w * 32 + i]) : x);
             }
           }
-          const float y_new = fmaxf(y_ref, my), al = ex2(y_ref - y_new);
+          const float y_new = fmaxf(y_ref, my - BELOW<FP8>), al = ex2(y_ref - y_new);
           l_sum *= al;
           if (j > 0) {
             // O may change once P_(j-1) V_(j-1) is in it

@@ -789,6 +789,37 @@ def test_values_of_scale_zero_come_first(G):
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("H_kv,G,per,listed", [(8, 4, 80, True), (1, 40, 148, True), (1, 16, 1184, False)])
+@pytest.mark.parametrize("at", [0, 100])
+def test_many_small_weights_beside_a_large_one(e4m3, H_kv, G, per, listed, at):
+    """One token of value 0 holds nearly all of the weight and 128K tokens 17.4 nats below it the rest, all of value 1:
+    the result is their share of the sum."""
+    L = 1 << 17
+    c = Case(e4m3, 64, H_kv, G, lens=(L,), per=(per,), seed=49, slack=0)
+    one = 0x38 if e4m3 else 1.0                        # 1 in e4m3
+    c.k.zero_()
+    c.v.fill_(one)
+    c.k[0, at, :, 0] = one
+    c.v[0, at] = 0
+    if e4m3:
+        c.ks.fill_(1.0)
+        c.vs.fill_(1.0)
+    c.q.zero_()
+    c.q[:, :, 0] = 17.375
+    if listed:
+        c.topk = torch.arange(L, device=DEV).int().expand(per, L).contiguous()
+    out, lse = c.run(scale=1.0, check=False)
+    # the output's half step; weights that lose at most 2^-11 (f16) or 2^-8 (bf16) of themselves, in f16 up to 2^-32 of
+    # the largest (2^-25 of 2^7); sums in L / 16 products of 16 tokens, each off by 2^-23 of what is there
+    share = (L - 1) * math.exp(-17.375)
+    exact = share / (1 + share)
+    tol = exact * (BF16 + (2.0 ** -11 if e4m3 else BF16) + L / 16 * 2.0 ** -23) + (L * 2.0 ** -32 if e4m3 else 0.0)
+    assert tol < exact / 32
+    assert bool(((out.double() - exact).abs() <= tol).all()), (exact, float(out.min()), float(out.max()))
+    assert bool(((lse.double() - 17.375 - math.log1p(share)).abs() <= 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("G,per", [(1, (37, 1, 1, 1)), (8, (60, 1, 0, 2))])
 def test_uneven_batches(e4m3, G, per):
     """More tiles than an even spread of the queries has."""
