@@ -450,7 +450,15 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
       auto logit = [&](auto m, float v, int n, int x, int y) {
         return m.value && !(((LIST ? have : vis[n][x]) >> (g + 8 * y)) & 1u) ? NEG_INF : v;
       };
-      auto weigh = [&](auto m) -> bool {  // m: std::true_type where something is masked
+      // A logit as the reference takes it, rounded.  Against an exact product a
+      // reference of 2^27 may be off by 2^3 and more: enough to overflow a weight.
+      auto rounded = [&](int n, int x, int y) {
+        const float v = s[n][y >> 1][2 * (y & 1) + x];
+        return __fmul_rn(FP8 ? __fmul_rn(v, ks[y]) : v, mul[n][x]);
+      };
+      // m: std::true_type where something is masked; again: behind a reference
+      // that has just moved
+      auto weigh = [&](auto m, auto again) -> bool {
         float top = 0.f;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -460,7 +468,8 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
           for (int y = 0; y < 2 * MTL; ++y) {
             const float s0 = s[n][y >> 1][2 * (y & 1)], s1 = s[n][y >> 1][2 * (y & 1) + 1];
             // (a row's factor last: its power of two and the token's scale may pass fp32's range between them)
-            const float2 v2 = FP8 ? unpair(fma2(mul2(pair(s0, s1), pair(ks[y], ks[y])), mul_2, ref_2))
+            const float2 v2 = again.value ? make_float2(rounded(n, 0, y) - y_ref[n][0], rounded(n, 1, y) - y_ref[n][1])
+                              : FP8 ? unpair(fma2(mul2(pair(s0, s1), pair(ks[y], ks[y])), mul_2, ref_2))
                                   : make_float2(fmaf(s0, mul[n][0], -y_ref[n][0]), fmaf(s1, mul[n][1], -y_ref[n][1]));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -478,10 +487,8 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
         }
         return __any_sync(0xffffffffu, top > LAZY<FP8>);
       };
-      for (bool again = false;; again = true) {
-        const bool above = masked ? weigh(std::true_type()) : weigh(std::false_type());
-        // (the first visible token always comes out above)
-        if (again || !above) break;
+      // (the first visible token always comes out above)
+      if (masked ? weigh(std::true_type(), std::false_type()) : weigh(std::false_type(), std::false_type())) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -489,17 +496,17 @@ __global__ void __launch_bounds__(F::THREADS, F::CTAS)
             float my = NEG_INF;
 #pragma unroll
             for (int y = 0; y < 2 * MTL; ++y)
-              my = fmaxf(my, logit(std::true_type(), s[n][y >> 1][2 * (y & 1) + x] * ks[y] * mul[n][x], n, x, y) +
-                                 (FP8 ? log2_scale(vs[y]) : 0.f));
+              my = fmaxf(my, logit(std::true_type(), reference<FP8>(rounded(n, x, y), vs[y]), n, x, y));
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, b));
-            const float y_new = fmaxf(y_ref[n][x], my - BELOW<FP8>);
+            const float y_new = fmaxf(y_ref[n][x], my);
             const float al = ex2(y_ref[n][x] - y_new);
             l_sum[n][x] *= al;
 #pragma unroll
             for (int j = 0; j < KT; ++j) o[j][n][x] *= al, o[j][n][2 + x] *= al;
             y_ref[n][x] = y_new;
           }
+        weigh(std::true_type(), std::true_type());
       }
       uint32_t pb[NR][2 * MTL];
 #pragma unroll

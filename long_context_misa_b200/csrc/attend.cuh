@@ -70,6 +70,16 @@ __device__ __forceinline__ float finite_max(float m, float x) {
 // reference out of fp32's range.
 __device__ __forceinline__ float log2_scale(float s) { return __log2f(fminf(fmaxf(s, 0x1p-93f), 0x1p100f)); }
 
+// The reference that a visible token of logit x and value scale vs asks for.
+// From 2^24 on an fp32 reference has no room for more than the logit: the
+// scale's power of two, rounded away or up, could cost or overflow the weight.
+template <bool FP8>
+__device__ __forceinline__ float reference(float x, float vs) {
+  if (!FP8) return x;
+  const float y = x + (log2_scale(vs) - BELOW<true>);
+  return fabsf(x) < 0x1p24f ? y : x;
+}
+
 // Prefix length of query i (0 for none) and its sequence (-1: outside the
 // cache, it sees nothing).
 __device__ __forceinline__ int attend_prefix(const KvView &c, const AttendView &a, int i, int *seq) {

@@ -584,7 +584,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
         const float *ks = scales.k[FP8 ? slot : 0] + g * HALF, *vs = scales.v[FP8 ? slot : 0] + g * HALF;
 
         uint32_t pk[HALF / 2];  // P as it goes back to tensor memory
-        auto weigh = [&](auto mk, float &sum) -> float {
+        // mk: std::true_type where something is masked; again: behind a
+        // reference that has just moved.  Then logits are rounded as it took
+        // them: against an exact product a reference of 2^27 may be off by 2^3
+        // and more, enough to overflow a weight.
+        auto weigh = [&](auto mk, auto again, float &sum) -> float {
           float top = 0.f;
           uint64_t s2[2] = {0u, 0u};  // (pairs of fp32)
           const uint64_t mul_2 = pair(mul, mul), ref_2 = pair(-y_ref, -y_ref);
@@ -613,6 +617,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
                 // (the row's factor last: its power of two and a token's scale may pass fp32's range between them)
                 if (FP8) x2 = mul2(x2, u ? pair(k4.z, k4.w) : pair(k4.x, k4.y));
                 float2 x = unpair(fma2(x2, mul_2, ref_2));
+                if (again.value) {  // (one by one: a paired product and its sum come out as one operation)
+                  x = unpair(x2);
+                  x.x = __fadd_rn(__fmul_rn(x.x, mul), -y_ref), x.y = __fadd_rn(__fmul_rn(x.y, mul), -y_ref);
+                }
                 const bool seen0 = !mk.value || ((see[w] >> (i + u)) & 1u), seen1 = !mk.value || ((see[w] >> (i + u + 1)) & 1u);
                 if (mk.value) x.x = seen0 ? x.x : NEG_INF, x.y = seen1 ? x.y : NEG_INF;
                 const float2 p = make_float2(ex2(x.x), ex2(x.y));
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
           return FP8 && sum > SUM_MAX ? 2.f * LAZY<FP8> : top;
         };
         float sum = 0.f, top = 2.f * LAZY<FP8>;
-        if (j > 0) top = masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
+        if (j > 0) top = masked ? weigh(std::true_type(), std::false_type(), sum) : weigh(std::false_type(), std::false_type(), sum);
         if (__any_sync(0xffffffffu, top > LAZY<FP8>)) {
           float my = NEG_INF;
 #pragma unroll 1
@@ -644,11 +652,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             const uint32_t sw = w == 0 ? see[0] : see[1];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = __uint_as_float(v[i]) * (FP8 ? ks[w * 32 + i] : 1.f) * mul;
-              if ((sw >> i) & 1u) my = fmaxf(my, FP8 ? x + log2_scale(vs[w * 32 + i]) : x);
+              const float x = __fmul_rn(FP8 ? __fmul_rn(__uint_as_float(v[i]), ks[w * 32 + i]) : __uint_as_float(v[i]), mul);
+              if ((sw >> i) & 1u) my = fmaxf(my, reference<FP8>(x, FP8 ? vs[w * 32 + i] : 1.f));
             }
           }
-          const float y_new = fmaxf(y_ref, my - BELOW<FP8>), al = ex2(y_ref - y_new);
+          const float y_new = fmaxf(y_ref, my), al = ex2(y_ref - y_new);
           l_sum *= al;
           if (j > 0) {
             // O may change once P_(j-1) V_(j-1) is in it
@@ -672,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(KvView c, Atten
             st_wait();
           }
           y_ref = y_new;
-          masked ? weigh(std::true_type(), sum) : weigh(std::false_type(), sum);
+          masked ? weigh(std::true_type(), std::true_type(), sum) : weigh(std::false_type(), std::true_type(), sum);
         }
         l_sum += sum;
 #pragma unroll

@@ -703,6 +703,33 @@ def test_logits_of_minus_infinity():
     assert float((out[0, 0].double() - want).abs().max()) < 6 * 2 * BF16
 
 
+@pytest.mark.parametrize("G", [3, 8, 20, 40])
+@pytest.mark.parametrize("k", [0, 64])
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("up", [16, 18, 20, 22, 24, 26, 40, 60, 100])
+def test_logits_beyond_their_own_precision(e4m3, G, k, up):
+    """Logits so large that half a step of theirs is a power of ten of weight: the largest takes all."""
+    c = Case(e4m3, 128, 1, G, lens=(300,), per=(2,), k=k, seed=50)
+    for f in (min(up, 60), up - min(up, 60)):
+        c.q *= 2.0 ** f
+    out, lse = c.run(check=False)
+    for i in range(c.n):
+        (kc, ks), (vc, vs) = c.rows64(i)
+        q = c.q[i].double()
+        s = torch.einsum("gd,td->gt", q, kc[:, 0] * ks) * 128 ** -0.5
+        E = (torch.einsum("gd,td->gt", q.abs(), kc[:, 0].abs() * ks) * 128 ** -0.5).amax(-1)
+        delta = (128 + 8) * 2.0 ** -23 * E + 2.0 ** -22 * (s.abs().amax(-1) + 1)
+        two = s.topk(2, dim=-1)
+        clear = two.values[:, 0] - two.values[:, 1] > 2 * delta + 200
+        assert up < 60 or bool(clear.any())
+        assert bool(((lse[i].double() - two.values[:, 0]).abs() <= delta + 6 + 2.0 ** -23 * s.abs().amax(-1)).all())
+        assert bool(torch.isfinite(out[i].float()).all())
+        v = vc[two.indices[:, 0], 0] * vs[two.indices[:, 0]]
+        # one value, its weight and its sum alike but for roundings of the weight, the quotient and the output
+        tol = (BF16 + (2.0 ** -11 if e4m3 else BF16) + 2.0 ** -20) * v.abs() + (2.0 ** -25 * 448 if e4m3 else 0.0)
+        assert bool(((out[i].double() - v).abs() <= tol)[clear].all())
+
+
 @pytest.mark.parametrize("G", [3, 20, 40])
 @pytest.mark.parametrize("k", [0, 64])
 def test_queries_of_any_magnitude(G, k):
