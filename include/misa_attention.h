@@ -127,11 +127,11 @@ typedef struct {
  * queries, its new index keys, its attention queries).  Rows that start on 16
  * bytes with rot a multiple of 16 and first and d multiples of 8 go through
  * 16-byte accesses; others are handled element by element.
- * Errors: MISA_ERR_INVALID for NULL pointers, n or H < 0, rot odd or outside
- * [2, d - first], first < 0, an unknown layout, a non-finite amplitude, a
- * group count outside [1, MISA_MAX_ROPE_GROUPS], in place with other strides,
- * rows of y whose strides let them meet, groups of which one starts where
- * another writes; MISA_ERR_UNSUPPORTED for d > 1024.
+ * Errors: MISA_ERR_INVALID for n or H < 0, rot odd or outside [2, d - first],
+ * first < 0, an unknown layout, a non-finite amplitude, a group count outside
+ * [1, MISA_MAX_ROPE_GROUPS], and in groups that have rows NULL pointers, in place
+ * with other strides, rows of y whose strides let them meet, groups of which one
+ * starts where another writes; MISA_ERR_UNSUPPORTED for d > 1024.
  */
 MISA_API misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups, int32_t n_groups,
                                      misa_stream stream);
@@ -184,8 +184,9 @@ MISA_API misa_status misa_append_kv(const misa_kv *kv, const misa_new_kv *new_kv
  *   k_out, v_out [n][k][H_kv][d] bf16 bit patterns, 16-byte aligned; one of
  *   them may be NULL
  * Tokens at and beyond seq_len (drafted ones) are read as they are.
- * Errors: those of the cache; MISA_ERR_INVALID for n < 0, k < 1, NULL seq or
- * tok, both outputs NULL or overlapping; MISA_ERR_UNSUPPORTED for k > MISA_MAX_L.
+ * Errors: those of the cache; MISA_ERR_INVALID for n < 0, k < 1, (n > 0) NULL seq
+ * or tok, both outputs NULL or overlapping; MISA_ERR_UNSUPPORTED for k >
+ * MISA_MAX_L.
  */
 MISA_API misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *tok, int32_t n, int32_t k,
                                   uint16_t *k_out, uint16_t *v_out, misa_stream stream);
@@ -250,10 +251,10 @@ typedef struct {
  * f16: contributions below 2^-21 of a row's largest are off by up to 2^-32 of it.
  * Workspace: misa_attend_workspace_bytes(kv, qs, k, draft ? draft->n : 0),
  * 16-byte aligned.  Results do not depend on what it held.
- * Errors: those of the cache; MISA_ERR_INVALID for NULL q/q_seq/q_pos/out,
- * n_q outside [0, 65535], H not a positive multiple of H_kv, a non-finite
- * scale, out that overlaps q, k < 1 with a list or k != 0 without one, a draft with NULL pointers
- * or n < 1; MISA_ERR_UNSUPPORTED for H > MISA_MAX_H, k > MISA_MAX_L, draft->n
+ * Errors: those of the cache; MISA_ERR_INVALID for n_q outside [0, 65535], H not
+ * a positive multiple of H_kv, a non-finite scale, k < 1 with a list, a draft of
+ * n < 1, and with n_q > 0 NULL q/q_seq/q_pos/out, k != 0 without a list, a draft
+ * with NULL pointers, out that overlaps q; MISA_ERR_UNSUPPORTED for H > MISA_MAX_H, k > MISA_MAX_L, draft->n
  * > MISA_MAX_DRAFT; MISA_ERR_WORKSPACE for a short workspace.
  */
 MISA_API misa_status misa_attend(const misa_kv *kv, const misa_attend_queries *qs, const int32_t *topk, int32_t k,

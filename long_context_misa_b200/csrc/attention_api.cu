@@ -141,13 +141,14 @@ misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups,
     if (g.n < 0 || g.H < 0 || g.d < 1) return fail(MISA_ERR_INVALID, "group %d: n=%d H=%d d=%d", i, g.n, g.H, g.d);
     if (g.d > 1024) return fail(MISA_ERR_UNSUPPORTED, "group %d: d=%d above 1024", i, g.d);
     if ((st = check_rope(rope, g.d)) != MISA_OK) return st;
-    if (g.n > 0 && g.H > 0 && (!g.x || !g.y || !g.pos)) return fail(MISA_ERR_INVALID, "group %d: x/y/pos is NULL", i);
+    if (g.n == 0 || g.H == 0) continue;  // nothing to read or write
+    if (!g.x || !g.y || !g.pos) return fail(MISA_ERR_INVALID, "group %d: x/y/pos is NULL", i);
     if (g.x == g.y && (g.x_row != g.y_row || g.x_head != g.y_head))
       return fail(MISA_ERR_INVALID, "group %d: in place needs equal strides", i);
     if (!apart(g.y_row, g.n, g.y_head, g.H, g.d)) return fail(MISA_ERR_INVALID, "group %d: rows of y overlap", i);
     for (int j = 0; j < i; ++j) {
       const misa_rope_rows &o = groups[j];
-      if (g.y && (g.y == o.y || g.y == o.x || g.x == o.y) && g.n > 0 && g.H > 0 && o.n > 0 && o.H > 0)
+      if ((g.y == o.y || g.y == o.x || g.x == o.y) && o.n > 0 && o.H > 0)
         return fail(MISA_ERR_INVALID, "groups %d and %d: one writes what the other takes", j, i);
     }
   }
@@ -183,7 +184,7 @@ misa_status misa_read_kv(const misa_kv *kv, const int32_t *seq, const int32_t *t
   if (st != MISA_OK) return st;
   if (n < 0 || k < 1) return fail(MISA_ERR_INVALID, "n=%d k=%d", n, k);
   if (k > MISA_MAX_L) return fail(MISA_ERR_UNSUPPORTED, "k=%d above %d", k, MISA_MAX_L);
-  if (!k_out && !v_out) return fail(MISA_ERR_INVALID, "k_out and v_out are both NULL");
+  if (n > 0 && !k_out && !v_out) return fail(MISA_ERR_INVALID, "k_out and v_out are both NULL");
   if (n > 0 && (!seq || !tok)) return fail(MISA_ERR_INVALID, "seq/tok is NULL");
   if (!aligned16(k_out) || !aligned16(v_out)) return fail(MISA_ERR_INVALID, "k_out and v_out must be 16-byte aligned");
   if (k_out && v_out && overlap16(k_out, v_out, (int64_t)n * k * kv->H_kv * kv->d))
@@ -204,12 +205,13 @@ misa_status misa_attend(const misa_kv *kv, const misa_attend_queries *qs, const 
   NvtxRange nvtx("misa_attend");
   misa_status st = check_attend(kv, qs, k, draft ? draft->n : 0);
   if (st != MISA_OK) return st;
-  if ((topk != nullptr) != (k > 0)) return fail(MISA_ERR_INVALID, "k=%d %s a list", k, topk ? "with" : "without");
-  if (draft && (draft->n < 1 || !draft->start || !draft->mask))
+  const bool any = qs->n_q > 0;  // an empty batch has no memory to point to
+  if (topk ? k < 1 : any && k > 0) return fail(MISA_ERR_INVALID, "k=%d %s a list", k, topk ? "with" : "without");
+  if (draft && (draft->n < 1 || (any && (!draft->start || !draft->mask))))
     return fail(MISA_ERR_INVALID, "draft n=%d, start or mask NULL", draft->n);
-  if (qs->n_q > 0 && (!qs->q || !qs->q_seq || !qs->q_pos || !out))
+  if (any && (!qs->q || !qs->q_seq || !qs->q_pos || !out))
     return fail(MISA_ERR_INVALID, "q/q_seq/q_pos/out is NULL");
-  if (qs->n_q > 0 && overlap16(qs->q, out, (int64_t)qs->n_q * qs->H * kv->d))
+  if (any && overlap16(qs->q, out, (int64_t)qs->n_q * qs->H * kv->d))
     return fail(MISA_ERR_INVALID, "out overlaps q");
   if (!std::isfinite(qs->scale)) return fail(MISA_ERR_INVALID, "scale is not finite");
   if (!aligned16(qs->q) || !aligned16(out)) return fail(MISA_ERR_INVALID, "q and out must be 16-byte aligned");

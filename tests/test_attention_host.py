@@ -203,6 +203,21 @@ def test_attend_refusals():
     assert L.misa_attend(by(kv()), None, FAKE, 4, None, FAKE, None, FAKE, 1 << 30, None) == INV
 
 
+def test_empty_batches_have_no_memory():
+    """Nothing to do is done whatever the pointers: torch gives an empty tensor's as 0."""
+    none = queries(n_q=0, q=None, q_seq=None, q_pos=None)
+    for d in (None, draft(start=None, mask=None), draft(mask=None)):
+        for k in (0, 4):
+            assert L.misa_attend(by(kv()), by(none), None, k, by(d) if d else None, None, None, None, 0, None) == M.MISA_OK
+    assert L.misa_attend(by(kv()), by(none), FAKE, 0, None, None, None, None, 0, None) == INV
+    assert L.misa_attend(by(kv()), by(none), None, 4, by(draft(n=0)), None, None, None, 0, None) == INV
+    assert L.misa_read_kv(by(kv()), None, None, 0, 3, None, None, None) == M.MISA_OK
+    assert L.misa_read_kv(by(kv()), None, None, 0, 0, None, None, None) == INV
+    for g in (rows(n=0, x=None, y=None, pos=None, y_row=1024), rows(H=0, x=None, y=None, x_head=64, y_head=64, n=2)):
+        assert L.misa_apply_rope(by(rope()), by(g), 1, None) == M.MISA_OK
+        assert L.misa_apply_rope(by(rope(rot=3)), by(g), 1, None) == INV
+
+
 def test_injected_failures():
     M.debug_fail_next(4)
     try:

@@ -519,6 +519,21 @@ def test_empty_sequence_and_empty_batch(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
+def test_calls_on_nothing(e4m3):
+    """An empty batch with a list, a draft or both; nothing to read back, nothing to rotate."""
+    for k, drafts in ((8, 0), (0, 5), (8, 40)):
+        c = Case(e4m3, 64, 2, 2, lens=(10,), per=(0,), k=k, drafts=drafts, seed=33)
+        out, lse = c.run()
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    ko, vo = A.read_kv(c.kv, ints([]), ints([]).view(0, 7))
+    assert ko.shape == vo.shape == (0, 7, 2, 64)
+    wide = torch.zeros(5, 3, 128, dtype=torch.bfloat16, device=DEV)
+    A.apply_rope(A.Rope(64), [(wide[:0, ::2], ints([]), torch.zeros(0, 2, 128, dtype=torch.bfloat16, device=DEV)),
+                              (wide[:, :0], torch.zeros(5, dtype=torch.int32, device=DEV), wide[:, :0])])
+    assert c.kv.device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("G", [3, 40])
 def test_lists_without_entries(e4m3, G):
     """A list of nothing shows the drafted tokens alone; without them nothing."""
