@@ -208,31 +208,44 @@ class Queries:
 class Workspace:
     """Grow-only device scratch buffer for the calls that need one.
 
-    A buffer that was outgrown stays allocated: a captured graph may still
-    hold its address."""
+    A buffer that was outgrown is dropped, unless it was handed out to a
+    captured graph, which may still hold its address, or to another stream
+    than the one it belongs to, where a call may still be using it.  Those
+    stay allocated in ``outgrown``, and the next one is half as large again at
+    the least, so that together they stay below twice the size in use."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
         self.outgrown = []
+        self._keep, self._home = False, None
 
-    def get(self, nbytes: int) -> torch.Tensor:
-        if self.buf.numel() < nbytes:
-            if self.buf.numel():
-                self.outgrown.append(self.buf)
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        return self.buf
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """At least nbytes for a call on ``stream`` (default: the current one)."""
+        buf = self.buf
+        here = torch._C._cuda_getCurrentRawStream(buf.device.index) if buf.is_cuda else None
+        if buf.numel() < nbytes:
+            size = max(nbytes, 256)
+            if self._keep:
+                self.outgrown.append(buf)
+                size = max(size, buf.numel() * 3 // 2)
+            self.buf = buf = torch.empty(size, dtype=torch.uint8, device=self.device)
+            self._keep, self._home = False, here
+        if not self._keep and here is not None:
+            at = here if stream is None else _stream(stream)
+            self._keep = at != self._home or at != here or torch.cuda.is_current_stream_capturing()
+        return buf
 
 
 def workspace_bytes(op: int, cache: KeyCache, qs: Queries, h: int = 0, k: int = 0, k_prime: int = 0) -> int:
     return int(_lib.misa_workspace_bytes(op, ctypes.byref(cache.struct), ctypes.byref(qs.struct), h, k, k_prime))
 
 
-def _ws(ws: Optional[Workspace], nbytes: int, device):
+def _ws(ws: Optional[Workspace], nbytes: int, device, stream):
     if nbytes == 0:
         return None, 0
     ws = ws or Workspace(device)
-    return ws.get(nbytes), nbytes
+    return ws.get(nbytes, stream), nbytes
 
 
 def pool_keys(cache: KeyCache, new_keys: Optional[torch.Tensor] = None, new_scale: Optional[torch.Tensor] = None,
@@ -261,7 +274,7 @@ def route_heads(cache: KeyCache, qs: Queries, h: int, heads: Optional[torch.Tens
     dev = qs.q.device
     if heads is None:
         heads = torch.empty(qs.n_q, h, dtype=torch.int32, device=dev)
-    buf, nb = _ws(ws, workspace_bytes(OP_ROUTE, cache, qs, h), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_ROUTE, cache, qs, h), dev, stream)
     args = (ctypes.byref(cache.struct), ctypes.byref(qs.struct), h)
     tail = (_ptr(heads), _ptr(router_scores), _ptr(buf), nb, _stream(stream))
     if agg == AGG_ABS_SUM:
@@ -278,7 +291,7 @@ def score_topk(cache: KeyCache, qs: Queries, heads: torch.Tensor, k: int, topk: 
     h = int(heads.shape[1])
     if topk is None:
         topk = torch.empty(qs.n_q, k, dtype=torch.int32, device=dev)
-    buf, nb = _ws(ws, workspace_bytes(OP_SCORE_TOPK, cache, qs, h, k), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_SCORE_TOPK, cache, qs, h, k), dev, stream)
     _check(_lib.misa_score_topk(ctypes.byref(cache.struct), ctypes.byref(qs.struct), _ptr(heads), h, k,
                                 _ptr(topk), _ptr(scores_out), _ptr(buf), nb, _stream(stream)))
     return topk
@@ -290,7 +303,7 @@ def dense_score_topk(cache: KeyCache, qs: Queries, k: int, topk: Optional[torch.
     dev = qs.q.device
     if topk is None:
         topk = torch.empty(qs.n_q, k, dtype=torch.int32, device=dev)
-    buf, nb = _ws(ws, workspace_bytes(OP_DENSE_TOPK, cache, qs, qs.H, k), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_DENSE_TOPK, cache, qs, qs.H, k), dev, stream)
     _check(_lib.dsa_dense_score_topk(ctypes.byref(cache.struct), ctypes.byref(qs.struct), k, _ptr(topk),
                                      _ptr(scores_out), _ptr(buf), nb, _stream(stream)))
     return topk
@@ -303,7 +316,7 @@ def rerank_topk(cache: KeyCache, qs: Queries, cand: torch.Tensor, k: int, topk: 
     k_prime = int(cand.shape[1])
     if topk is None:
         topk = torch.empty(qs.n_q, k, dtype=torch.int32, device=dev)
-    buf, nb = _ws(ws, workspace_bytes(OP_RERANK_TOPK, cache, qs, 0, k, k_prime), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_RERANK_TOPK, cache, qs, 0, k, k_prime), dev, stream)
     _check(_lib.misa_rerank_topk(ctypes.byref(cache.struct), ctypes.byref(qs.struct), _ptr(cand), k_prime, k,
                                  _ptr(topk), _ptr(scores_out), _ptr(buf), nb, _stream(stream)))
     return topk
@@ -316,7 +329,7 @@ def dagger_topk(cache: KeyCache, qs: Queries, heads: torch.Tensor, k_prime: int,
     h = int(heads.shape[1])
     if topk is None:
         topk = torch.empty(qs.n_q, k, dtype=torch.int32, device=dev)
-    buf, nb = _ws(ws, workspace_bytes(OP_DAGGER_TOPK, cache, qs, h, k, k_prime), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_DAGGER_TOPK, cache, qs, h, k, k_prime), dev, stream)
     _check(_lib.misa_dagger_topk(ctypes.byref(cache.struct), ctypes.byref(qs.struct), _ptr(heads), h, k_prime, k,
                                  _ptr(topk), _ptr(buf), nb, _stream(stream)))
     return topk
@@ -332,7 +345,7 @@ def dagger_decode(cache: KeyCache, qs: Queries, new_keys: torch.Tensor, new_scal
     if topk is None:
         topk = torch.empty(qs.n_q, k, dtype=torch.int32, device=dev)
     count = int(new_keys.shape[1])
-    buf, nb = _ws(ws, workspace_bytes(OP_DAGGER_DECODE, cache, qs, h, k, k_prime), dev)
+    buf, nb = _ws(ws, workspace_bytes(OP_DAGGER_DECODE, cache, qs, h, k, k_prime), dev, stream)
     _check(_lib.misa_dagger_decode(ctypes.byref(cache.struct), ctypes.byref(qs.struct), _ptr(new_keys),
                                    _ptr(new_scale), _ptr(new_pos), count, h, k_prime, k, _ptr(heads), _ptr(topk),
                                    _ptr(buf), nb, _stream(stream)))

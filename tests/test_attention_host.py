@@ -218,6 +218,13 @@ def test_empty_batches_have_no_memory():
         assert L.misa_apply_rope(by(rope(rot=3)), by(g), 1, None) == INV
 
 
+def test_a_growing_workspace_keeps_nothing():
+    ws = M.Workspace("cpu")
+    for n in range(1000, 100000, 1000):
+        assert ws.get(n).numel() == n
+    assert ws.get(5).numel() == 99000 and ws.outgrown == []
+
+
 def test_injected_failures():
     M.debug_fail_next(4)
     try:

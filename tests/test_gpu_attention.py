@@ -959,6 +959,32 @@ def test_streams_and_graphs():
     c.check(graphs[0][1], graphs[0][2])
 
 
+def test_workspaces_keep_what_others_may_still_use():
+    """Outgrown buffers stay for graphs and other streams, together below twice the one in use; else they are dropped."""
+    ws = M.Workspace(DEV)
+    for n in range(1 << 20, 1 << 24, 1 << 18):
+        assert ws.get(n).numel() == n
+    assert ws.outgrown == []
+    side = torch.cuda.Stream()
+    held = []
+    for n in range(1 << 24, 1 << 27, 1 << 20):
+        way = (n >> 20) % 3
+        if way == 0:
+            held.append(ws.get(n, stream=side).data_ptr())
+        elif way == 1:
+            with torch.cuda.stream(side):
+                ws.get(n)                              # (its own where it grows here: torch's allocator sees to that)
+        else:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                buf = ws.get(n)
+                buf[:1].zero_()
+            held.append(buf.data_ptr())
+    have = {b.data_ptr() for b in ws.outgrown} | {ws.buf.data_ptr()}
+    assert set(held) <= have and len(ws.outgrown) < 12
+    assert sum(b.numel() for b in ws.outgrown) <= 2 * ws.buf.numel()
+
+
 def test_same_call_same_bits():
     c = Case(False, 128, 4, 4, lens=(30000, 777), per=(3, 2), seed=52)
     a = c.run()
