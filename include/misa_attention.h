@@ -108,8 +108,9 @@ MISA_API misa_status misa_rope_phases(uint64_t *phases, int32_t rot, double base
  * A tensor of rows to rotate: x and y are bf16 bit patterns [n][H][d] with the
  * given strides in elements between rows and between heads (the d elements of
  * a head are consecutive); pos [n] int32, any value, is each row's position.
- * y may be x with equal strides (in place); other overlaps are not allowed,
- * rows of y that share memory and groups that write the same rows among them.
+ * y may be x with equal strides (in place); other overlaps are refused: rows of
+ * y that share memory with one another, with rows of x or with another group's
+ * rows.  Interleaved slices of one projection do not.
  */
 typedef struct {
   const uint16_t *x;
@@ -130,8 +131,8 @@ typedef struct {
  * Errors: MISA_ERR_INVALID for n or H < 0, rot odd or outside [2, d - first],
  * first < 0, an unknown layout, a non-finite amplitude, a group count outside
  * [1, MISA_MAX_ROPE_GROUPS], and in groups that have rows NULL pointers, in place
- * with other strides, rows of y whose strides let them meet, groups of which one
- * starts where another writes; MISA_ERR_UNSUPPORTED for d > 1024.
+ * with other strides, rows of y whose strides let them meet, or that share
+ * memory with rows of x or of another group; MISA_ERR_UNSUPPORTED for d > 1024.
  */
 MISA_API misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups, int32_t n_groups,
                                      misa_stream stream);
@@ -254,7 +255,8 @@ typedef struct {
  * Errors: those of the cache; MISA_ERR_INVALID for n_q outside [0, 65535], H not
  * a positive multiple of H_kv, a non-finite scale, k < 1 with a list, a draft of
  * n < 1, and with n_q > 0 NULL q/q_seq/q_pos/out, k != 0 without a list, a draft
- * with NULL pointers, out that overlaps q; MISA_ERR_UNSUPPORTED for H > MISA_MAX_H, k > MISA_MAX_L, draft->n
+ * with NULL pointers, out, lse or the workspace that overlap one another or q;
+ * MISA_ERR_UNSUPPORTED for H > MISA_MAX_H, k > MISA_MAX_L, draft->n
  * > MISA_MAX_DRAFT; MISA_ERR_WORKSPACE for a short workspace.
  */
 MISA_API misa_status misa_attend(const misa_kv *kv, const misa_attend_queries *qs, const int32_t *topk, int32_t k,

@@ -169,7 +169,8 @@ def apply_rope(rope: Rope, rows: Sequence[Tuple[torch.Tensor, torch.Tensor, torc
     """Rotate up to four tensors in one launch.
 
     rows: (x, pos, out) triples; x and out are bf16 (or bf16 bits) [n][H][d] with consecutive elements along d and
-    any other strides, out may be x itself; pos is int32 [n].  Rows of one out, and the triples, must not meet.
+    any other strides, out may be x itself; pos is int32 [n].  Other rows that meet are refused: those of one out,
+    of out and x, of two triples.
     """
     if not 1 <= len(rows) <= MAX_ROPE_GROUPS:
         raise ValueError(f"apply_rope takes 1 to {MAX_ROPE_GROUPS} tensors, got {len(rows)}")

@@ -1,5 +1,6 @@
 // C ABI of the attention side: argument validation and dispatch.
 // Declarations and semantics: include/misa_attention.h.
+#include <algorithm>
 #include <cmath>
 
 #include "api_common.h"
@@ -47,8 +48,69 @@ bool apart(int64_t row, int n, int64_t head, int H, int d) {
   return rows_out || heads_out;
 }
 
+// [n][H] rows of d bytes: strides not negative, extents of 1 where they repeat
+// the same memory.
+struct Rows {
+  int64_t at, row, head, n, H, d;
+  Rows(const uint16_t *p, int64_t row_, int64_t head_, int n_, int H_, int d_)
+      : at((int64_t)(intptr_t)p), row(2 * row_), head(2 * head_), n(row_ ? n_ : 1), H(head_ ? H_ : 1), d(2 * (int64_t)d_) {
+    if (row < 0) at += row * (n - 1), row = -row;
+    if (head < 0) at += head * (H - 1), head = -head;
+    if (n == 1) row = 0;
+    if (H == 1) head = 0;
+  }
+  int64_t row_span() const { return head * (H - 1) + d; }
+  int64_t span() const { return row * (n - 1) + row_span(); }
+};
+
+// The whole numbers k of [lo, hi] with -below < off + k step < above; step > 0,
+// or 0 with lo == hi == 0.
+struct Range {
+  int64_t lo, hi;
+};
+Range within(int64_t off, int64_t step, int64_t below, int64_t above, int64_t lo, int64_t hi) {
+  if (step == 0) return off > -below && off < above ? Range{0, 0} : Range{0, -1};
+  auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+  return {std::max(lo, floor_div(-below - off, step) + 1), std::min(hi, -floor_div(off - above, step) - 1)};
+}
+
+// Whether a row of a and one of b share memory, b's first row `off` behind a's.
+bool rows_meet(const Rows &a, const Rows &b, int64_t off) {
+  for (int64_t p = 0; p < a.H; ++p) {
+    const Range q = within(off - p * a.head, b.head, b.d, a.d, 0, b.H - 1);
+    if (q.lo <= q.hi) return true;
+  }
+  return false;
+}
+
+// Whether two sets of rows share memory: exactly, so that interleaved slices of
+// one projection are told from rows that meet.
+bool meet(const Rows &a, const Rows &b) {
+  const int64_t off = b.at - a.at;
+  if (off >= a.span() || -off >= b.span()) return false;
+  if (a.row == b.row || a.n == 1 || b.n == 1) {  // rows k = j - i apart
+    const int64_t row = a.n == 1 ? b.row : a.row;
+    const Range k = within(off, row, b.row_span(), a.row_span(), 1 - a.n, b.n - 1);
+    for (int64_t i = k.lo; i <= k.hi; ++i)
+      if (rows_meet(a, b, off + i * row)) return true;
+    return false;
+  }
+  for (int64_t i = 0; i < a.n; ++i) {
+    const Range j = within(off - i * a.row, b.row, b.row_span(), a.row_span(), 0, b.n - 1);
+    for (int64_t x = j.lo; x <= j.hi; ++x)
+      if (rows_meet(a, b, off - i * a.row + x * b.row)) return true;
+  }
+  return false;
+}
+
 // Whether two arrays of n 16-bit elements share memory.
 bool overlap16(const uint16_t *a, const uint16_t *b, int64_t n) { return a < b + n && b < a + n; }
+
+// Whether two arrays of bytes do.
+bool share(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
 
 misa::KvView view(const misa_kv *c) {
   misa::KvView v;
@@ -146,9 +208,13 @@ misa_status misa_apply_rope(const misa_rope *rope, const misa_rope_rows *groups,
     if (g.x == g.y && (g.x_row != g.y_row || g.x_head != g.y_head))
       return fail(MISA_ERR_INVALID, "group %d: in place needs equal strides", i);
     if (!apart(g.y_row, g.n, g.y_head, g.H, g.d)) return fail(MISA_ERR_INVALID, "group %d: rows of y overlap", i);
+    const Rows x(g.x, g.x_row, g.x_head, g.n, g.H, g.d), y(g.y, g.y_row, g.y_head, g.n, g.H, g.d);
+    if (g.x != g.y && meet(x, y)) return fail(MISA_ERR_INVALID, "group %d: rows of y overlap rows of x", i);
     for (int j = 0; j < i; ++j) {
       const misa_rope_rows &o = groups[j];
-      if ((g.y == o.y || g.y == o.x || g.x == o.y) && o.n > 0 && o.H > 0)
+      if (o.n == 0 || o.H == 0) continue;
+      const Rows ox(o.x, o.x_row, o.x_head, o.n, o.H, o.d), oy(o.y, o.y_row, o.y_head, o.n, o.H, o.d);
+      if (meet(y, oy) || meet(y, ox) || meet(x, oy))
         return fail(MISA_ERR_INVALID, "groups %d and %d: one writes what the other takes", j, i);
     }
   }
@@ -218,6 +284,11 @@ misa_status misa_attend(const misa_kv *kv, const misa_attend_queries *qs, const 
   const size_t need = misa::attend_ws_bytes(view(kv), qs->n_q, qs->H, k, draft ? draft->n : 0);
   if (ws_bytes < need) return fail(MISA_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
   if (need > 0 && (!ws || !aligned16(ws))) return fail(MISA_ERR_INVALID, "workspace NULL or not 16-byte aligned");
+  const size_t n_lse = (size_t)qs->n_q * qs->H, n_row = n_lse * kv->d * 2;
+  if (share(lse, n_lse * 4, qs->q, n_row) || share(lse, n_lse * 4, out, n_row))
+    return fail(MISA_ERR_INVALID, "lse overlaps q or out");
+  if (share(ws, need, qs->q, n_row) || share(ws, need, out, n_row) || share(ws, need, lse, n_lse * 4))
+    return fail(MISA_ERR_INVALID, "the workspace overlaps q, out or lse");
   if (injected_failure("misa_attend", &st)) return st;
   misa::AttendView a;
   a.q = qs->q;

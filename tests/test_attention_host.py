@@ -146,6 +146,77 @@ def test_outputs_that_meet_are_refused():
         M.debug_fail_next(0)
 
 
+def _addresses(p, row, head, n, H, d):
+    return {p // 2 + i * row + h * head + e for i in range(n) for h in range(H) for e in range(d)}
+
+
+def test_rotated_rows_that_meet_are_refused_and_no_others():
+    """Random strides and offsets against the sets of elements themselves: in and out of one group, and of two."""
+    rng = np.random.default_rng(3)
+    good = bad = 0
+    base = 1 << 24
+
+    def strides(n, H, d):
+        if rng.integers(2):                            # heads inside rows, or the other way round
+            head = d + int(rng.integers(0, 7))
+            return head * (H - 1) + d + int(rng.integers(0, 3 * d)), head
+        row = d + int(rng.integers(0, 7))
+        return row, row * (n - 1) + d + int(rng.integers(0, 2 * d))
+
+    for _ in range(4000):
+        n, H, d = int(rng.integers(1, 6)), int(rng.integers(1, 4)), int(rng.choice([8, 16]))
+        m, J = int(rng.integers(1, 6)), int(rng.integers(1, 4))
+        (xr, xh), (yr, yh) = strides(n, H, d), strides(n, H, d)
+        if rng.integers(2):
+            yr, yh = xr, xh                            # slices of one projection
+        if rng.integers(6) == 0:
+            xr = 0                                     # one row for all
+        pr, ph = (xr, xh) if rng.integers(2) and xr else strides(m, J, d)
+        if rng.integers(8) == 0:
+            yr, yh = -yr, -yh
+        x = base
+        y = base + 2 * int(rng.integers(-120, 120))
+        z = base + 2 * int(rng.integers(-400, 400))
+        one = rows(x=x, y=y, x_row=xr, x_head=xh, y_row=yr, y_head=yh, n=n, H=H, d=d)
+        two = rows(x=z, y=z, x_row=pr, x_head=ph, y_row=pr, y_head=ph, n=m, H=J, d=d)
+        X, Y, Z = _addresses(x, xr, xh, n, H, d), _addresses(y, yr, yh, n, H, d), _addresses(z, pr, ph, m, J, d)
+        if len(Z) < m * J * d or len(Y) < n * H * d:
+            continue
+        in_place = x == y and (xr, xh) == (yr, yh)
+        first = x != y and bool(X & Y) or x == y and not in_place
+        both = first or bool(Z & (X | Y))
+        r = rope(rot=8)
+        for groups, meets in (((one,), first), ((one, two), both), ((two, one), both)):
+            M.debug_fail_next(1)
+            try:
+                st = L.misa_apply_rope(by(r), (A.misa_rope_rows * len(groups))(*groups), len(groups), None)
+            finally:
+                M.debug_fail_next(0)
+            assert st == (INV if meets else M.MISA_ERR_CUDA), (st, M.last_error(), n, H, d, xr, xh, yr, yh, y - x, pr, ph, z - x)
+            good, bad = good + (not meets), bad + meets
+    assert good > 1000 and bad > 1000
+
+
+def test_attention_outputs_that_meet_are_refused():
+    c, q = kv(L_cap=65536), queries(n_q=1)
+    need = L.misa_attend_workspace_bytes(by(c), by(q), 0, 0)
+    row, out, lse, ws = q.H * c.d * 2, 1 << 32, 1 << 33, 1 << 34
+
+    def call(out=out, lse=lse, ws=ws):
+        return L.misa_attend(by(c), by(q), None, 0, None, out, lse, ws, need, None)
+
+    M.debug_fail_next(7)
+    try:
+        for ok in (dict(), dict(lse=out + row), dict(lse=out - 4 * q.H), dict(ws=out + row), dict(ws=out - need),
+                   dict(lse=ws + need), dict(lse=None)):
+            assert call(**ok) == M.MISA_ERR_CUDA, ok
+    finally:
+        M.debug_fail_next(0)
+    for bad in (dict(lse=out), dict(lse=out + row - 4), dict(lse=q.q), dict(lse=q.q - 4 * q.H + 4), dict(ws=out + row - 16),
+                dict(ws=out - need + 16), dict(ws=q.q), dict(lse=ws), dict(lse=ws + need - 4)):
+        assert call(**bad) == INV, bad
+
+
 def test_host_tensors_are_refused():
     """Pointers to host memory never reach a kernel."""
     k = torch.zeros(1, 8, 1, 64, dtype=torch.bfloat16)
