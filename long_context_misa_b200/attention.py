@@ -359,7 +359,7 @@ def tree_mask(parents: Sequence[int], n: Optional[int] = None) -> torch.Tensor:
         if p >= 0:
             seen[j] = seen[p]
         seen[j, j] = 1
-    words = (seen.view(t, -1, 32) << torch.arange(32)).sum(-1)
+    words = (seen.view(t, seen.shape[1] // 32, 32) << torch.arange(32)).sum(-1)
     return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
 
 

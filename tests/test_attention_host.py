@@ -364,6 +364,12 @@ def test_tree_mask():
         A.tree_mask([-1, 0], n=1)
 
 
+def test_tree_mask_of_no_nodes():
+    """A sequence without drafted tokens has no rows of words."""
+    assert tuple(A.tree_mask([], n=40).shape) == (0, 2) and A.tree_mask([], n=40).dtype == torch.int32
+    assert tuple(A.tree_mask([]).shape) == (0, 0)
+
+
 def test_binding_refusals():
     k = torch.zeros(2, 16, 4, 128, dtype=torch.bfloat16)
     n = torch.zeros(2, dtype=torch.int32)
