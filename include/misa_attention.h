@@ -69,7 +69,8 @@ typedef struct {
  * in fp32, rounded once to the output's type.  The other elements are kept.
  *   phase  [rot/2] uint64, device memory (misa_rope_phases fills a host array).
  *          The product p * phase[i] wraps modulo 2^64, that is modulo whole
- *          turns, so an angle is exact to 2^-32 turns at every position.
+ *          turns, and its fraction of a turn is rounded to fp32: an angle is
+ *          off by at most 2^-26 turns, at every position.
  *   layout MISA_ROPE_HALF: pair i = elements (first + i, first + rot/2 + i);
  *          MISA_ROPE_INTERLEAVED: (first + 2i, first + 2i + 1).
  */

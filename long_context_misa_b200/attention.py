@@ -430,8 +430,11 @@ class SparseAttention:
     """The attention of a decode step around MISA-dagger (see misa.MisaDaggerDecode).
 
     ``before`` rotates the rows of ``rotate`` with ``rope`` (up to four (x, pos, out) triples in one launch: the
-    step's index queries, its new index keys, its attention queries) and writes new_k, new_v
+    step's index queries, its attention queries, the new keys of a bf16 index cache) and writes new_k, new_v
     [n_seq][1][H_kv][d] at new_pos, the keys rotated by ``kv_rope``; ``after`` attends over the step's top-k.
+    The new keys of an e4m3 index cache reach the step as codes.  Where they come as bf16 rows, rotate them
+    (apply_rope), write them with misa.append_keys_e4m3 before the step runs, and give the step itself positions of
+    -1, which append nothing; all of it can be captured together.  The step has no drafted tokens.
     All buffers are the caller's or allocated here once; out [n_q][H][d] and lse [n_q][H] hold the step's result.
     """
 

@@ -9,7 +9,8 @@ namespace misa {
 // turns / 2^64.  The 64-bit product wraps modulo whole turns, so no range
 // reduction is needed and the angle of position 262143 is as exact as that of
 // position 1 (an fp32 angle there would be off by 2^18 * 2^-24 = 2^-6
-// radians).  Its top 32 bits, rounded, are a signed fraction of a turn.
+// radians).  Its top 32 bits, rounded, are a signed fraction of a turn, which
+// sincospif takes as an fp32 number: up to 2^-26 turns off.
 __device__ __forceinline__ float2 rope_cos_sin(uint64_t phase, int p, float amplitude) {
   const uint64_t turns = phase * (uint64_t)(int64_t)p;
   const int f = (int)(uint32_t)((turns + 0x80000000ull) >> 32);

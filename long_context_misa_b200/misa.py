@@ -401,11 +401,11 @@ class MisaDaggerDecode:
     result in attention.out.
     """
 
-    # kernels of one step when the batch runs fused (decode shapes whose
-    # scoring grid fits on the device at once and whose k' candidates fit one
-    # thread-block cluster per query): the append (which also clears the
-    # counting words), routing + routed scoring + top-k', and the all-head
-    # re-rank with the final top-k
+    # kernels of one step without attention when the batch runs fused (decode
+    # shapes whose scoring grid fits on the device at once and whose k'
+    # candidates fit one thread-block cluster per query): the append (which
+    # also clears the counting words), routing + routed scoring + top-k', and
+    # the all-head re-rank with the final top-k
     LAUNCHES = 3
 
     def __init__(self, cache: KeyCache, qs: Queries, h: int, k_prime: int, k: int, new_keys: torch.Tensor,

@@ -1124,3 +1124,53 @@ def test_decode_step_with_its_attention():
     assert kv.device_status() == 0 and cache.device_status() == 0
     with pytest.raises(ValueError):
         A.SparseAttention(kv, aq, *new, pos, wl.k, rotate=[(raw_q, qs.q_pos, q)])
+
+
+def test_decode_step_over_e4m3_index_keys():
+    """The step of an e4m3 index cache: its new keys rotated and written before it in one graph, its own append left out
+    by positions of -1."""
+    from long_context_misa_b200 import inputs as G
+    wl = G.WORKLOADS["misa_dagger_decode_128k"].scaled(n_seq=2, L=8192, k=256, k_prime=1024, needles_per_seq=2)
+    inp = G.make_inputs(wl, 0)
+    cache, qs = M.device_inputs(inp)
+    n, H_kv, H, d = wl.n_seq, 2, 16, 128
+    g, pos, none = gen(71), ints((inp.seq_len - 1).tolist()), ints([-1] * wl.n_seq)
+    cache.seq_len.copy_(pos)
+    M.pool_keys(cache)
+    r = A.Rope(64, base=500000.0)
+    raw_iq, raw_ik = qs.q.clone().view(torch.bfloat16), randn(g, n, 1, 128).bfloat16()
+    ik, raw_q = torch.empty_like(raw_ik), randn(g, n, H, d).bfloat16()
+    q = torch.empty_like(raw_q)
+    kv = A.KVCache.empty(n, cache.L_cap, H_kv, d, True)
+    A.append_kv(kv, *(randn(g, n, cache.L_cap - 1, H_kv, d).bfloat16() for _ in range(2)), ints([0] * n), rope=r)
+    new = [randn(g, n, 1, H_kv, d).bfloat16() for _ in range(2)]
+    aq = A.AttentionQueries(q, qs.q_seq, qs.q_pos)
+    unused = torch.zeros(n, 1, 128, dtype=torch.uint8, device=DEV), torch.ones(n, 1, device=DEV)
+    step = M.MisaDaggerDecode(cache, qs, wl.h, wl.k_prime, wl.k, *unused, none,
+                              attention=A.SparseAttention(kv, aq, *new, pos, wl.k, kv_rope=r))
+
+    def whole():
+        A.apply_rope(r, [(raw_iq, qs.q_pos, qs.q.view(torch.bfloat16)), (raw_ik, pos, ik), (raw_q, qs.q_pos, q)])
+        M.append_keys_e4m3(cache, ik.view(torch.int16), pos)
+        step.run()
+    whole()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        whole()
+    for _ in range(2):
+        raw_iq.copy_(randn(g, *raw_iq.shape)), raw_ik.copy_(randn(g, *raw_ik.shape)), raw_q.copy_(randn(g, *raw_q.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_rope(ik, raw_ik, pos, r)
+        for s in range(n):
+            codes, scale = plain_codes(ik[s])
+            assert torch.equal(cache.keys[s, int(pos[s])], codes[0]) and torch.equal(cache.scale[s, int(pos[s])], scale[0])
+        assert cache.seq_len.tolist() == kv.seq_len.tolist() == inp.seq_len.tolist()
+        pool = cache.pool.clone()
+        M.pool_keys(cache)                             # the same means of 128 keys, summed in other groups
+        top = (cache.keys.view(torch.float8_e4m3fn).float() * cache.scale[..., None]).abs().max()
+        assert bool(((pool - cache.pool).abs() <= 2 * 128 * 2.0 ** -24 * top).all())
+        assert torch.equal(step.topk, M.dagger_topk(cache, qs, step.heads, wl.k_prime, wl.k))
+        want = A.attend(kv, aq, topk=step.topk, with_lse=True)
+        assert torch.equal(step.attention.out, want[0]) and torch.equal(step.attention.lse, want[1])
+    assert kv.device_status() == 0 and cache.device_status() == 0
