@@ -218,23 +218,27 @@ class Workspace:
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
         self.outgrown = []
-        self._keep, self._home = False, None
+        self._size, self._keep, self._home = 0, False, None
+        self._gpu = self.buf.device.index if self.buf.is_cuda else None
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         """At least nbytes for a call on ``stream`` (default: the current one)."""
-        buf = self.buf
-        here = torch._C._cuda_getCurrentRawStream(buf.device.index) if buf.is_cuda else None
-        if buf.numel() < nbytes:
+        grow = self._size < nbytes
+        if self._gpu is None or (self._keep and not grow):
+            here = None
+        else:
+            here = torch._C._cuda_getCurrentRawStream(self._gpu)
+        if grow:
             size = max(nbytes, 256)
             if self._keep:
-                self.outgrown.append(buf)
-                size = max(size, buf.numel() * 3 // 2)
-            self.buf = buf = torch.empty(size, dtype=torch.uint8, device=self.device)
-            self._keep, self._home = False, here
-        if not self._keep and here is not None:
+                self.outgrown.append(self.buf)
+                size = max(size, self._size * 3 // 2)
+            self.buf = torch.empty(size, dtype=torch.uint8, device=self.device)
+            self._size, self._keep, self._home = size, False, here
+        if here is not None:
             at = here if stream is None else _stream(stream)
-            self._keep = at != self._home or at != here or torch.cuda.is_current_stream_capturing()
-        return buf
+            self._keep = at != self._home or at != here or torch._C._cuda_isCurrentStreamCapturing()
+        return self.buf
 
 
 def workspace_bytes(op: int, cache: KeyCache, qs: Queries, h: int = 0, k: int = 0, k_prime: int = 0) -> int:

@@ -777,6 +777,8 @@ def test_rows_of_very_different_magnitude(e4m3, G, k):
     c.q[1, 1::3] *= 2.0 ** 12                          # heads of one query, 2^32 apart
     c.q[1, 2::3] *= 2.0 ** -20
     c.q[2] = 0
+    c.q[4] *= 2.0 ** 60
+    c.q[4] *= 2.0 ** 40                                # one at 2^100
     c.pos[5] = -1                                      # padding: sees nothing
     c.q[5] = 3e38
     if k:
