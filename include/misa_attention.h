@@ -45,7 +45,8 @@ extern "C" {
  *   seq_len  [n_seq]                  int32 committed tokens per sequence
  *   status   [1] uint32 or NULL       device error bits (MISA_DEV_*)
  * dtype is a misa_key_dtype.  Supported: d = 64 or 128, 1 <= H_kv <= 128,
- * L_cap <= MISA_MAX_L.
+ * L_cap <= MISA_MAX_L.  Keys and values have the same width d: a cache of one
+ * latent row per token, whose values are a part of wider keys, is not supported.
  */
 typedef struct {
   void *k;

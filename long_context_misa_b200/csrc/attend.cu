@@ -24,18 +24,22 @@
 // memory, in a fixed order; more shares meet in the workspace, where
 // attend_combine_kernel joins them.
 //
-// Measured, heads of 128, e4m3.  Lists of 2048 tokens, 8 queries x 64 heads on
-// 8 key/value heads: 18.5 us, of which the stream of rows (35 MB) is about 8 and
-// the launch, the lists' look-up and the join of 8 shares the rest.  512
-// queries x 64 heads on 4: 196 us for 1.1 GB of gathered rows, and 128 x 64
-// on 8: 85 us for 0.56 GB; both are what the L2 gives to gathers of 128-byte
-// rows (5.5 to 6.6 TB/s): variants with more warps, with longer chunks and with
-// fewer instructions per chunk took the same time; issue slots are 41 % busy,
-// the tensor pipe 30 %.  Whole prefixes, 8 x 16K tokens, 4 heads per key/value
-// head: 62 us, 4.4 TB/s (bf16: 6.0 TB/s).
+// Measured, heads of 128, e4m3, calls one behind the other in a graph.  Lists of
+// 2048 tokens, 8 queries x 64 heads on 8 key/value heads: 15.4 us for 35 MB of
+// rows (5.3 us of HBM); the lists' look-up and the join of 8 shares come before
+// and after them.  512 queries x 64 heads on 4: 183 us for 1.1 GB of gathered
+// rows (6.0 TB/s), and 128 x 64 on 8: 80 us for 0.56 GB.  Nothing is saturated
+// there (128 queries, captured): L2 21 %, reads over the crossbar 17 %, L1 47 %,
+// mma.sync 32 %, issue slots 39 %; a scheduler has 1.8 warps, 0.48 of them
+// eligible, and the largest stall is the fixed latency of an instruction.  It is
+// the chain of a chunk's steps, with the 8 warps per SM that the registers of O
+// leave; forms with more warps, longer chunks and fewer instructions per chunk
+// took the same time.  Whole prefixes, 8 x 16K tokens, 4 heads per key/value
+// head: 58 us, 4.7 TB/s (bf16: 84 us, 6.4 TB/s).
 //
 // Numbers.  bf16 caches: bf16 products; the weights e^(s - ref) are rounded to
-// bf16 before they meet the values.  e4m3 caches: codes are exact in f16; each
+// bf16 before they meet the values (both sides of a product have one type, and
+// a second product for the lower halves would double the products of P V).  e4m3 caches: codes are exact in f16; each
 // row of queries is scaled by a power of two of its own into f16's range (bf16
 // has 8 significant bits, so elements down to 2^-23 of the row's largest stay
 // exact).  With ref 7 binary orders below the running maximum of
@@ -693,10 +697,14 @@ struct Plan {
 //
 // More than 16 rows without lists, or 32 with them, go to the tcgen05 kernel.
 // Measured on both (us, mma.sync / tcgen05; 8 sequences, 8 key/value heads of
-// 128): 12 rows over 16K bf16 tokens 89 / 92 and e4m3 74 / 137, 24 rows 152 / 93
-// and 249 / 137; 12 rows over 1000 tokens 20 / 20 and 21 / 28, 24 rows 29 / 21 and
-// 33 / 29; lists of 2048 tokens (2 key/value heads), 16 rows 10 / 15 and 11 / 21,
-// 32 rows 14 / 16 and 19 / 21.
+// 128, 4 heads each; more rows are more queries).  Over 16K tokens, bf16 then
+// e4m3: 12 rows 88 / 88 and 65 / 138, 16 rows 88 / 89 and 67 / 140, 20 rows 139 /
+// 90 and 110 / 140, 32 rows 142 / 91 and 112 / 142.  Over 1000 tokens: 16 rows
+// 15.8 / 16.4 and 16.8 / 25.0, 20 rows 19.5 / 16.8 and 19.9 / 25.2.  Lists of 2048
+// tokens (2 key/value heads): 16 rows 8.8 / 13.0 and 9.3 / 19.3, 32 rows 12.3 /
+// 13.5 and 13.8 / 19.5.  (17 to 32 rows over e4m3 prefixes would be faster as two
+// tiles of mma.sync, with up to 16 heads per key/value head; the rule does not
+// tell them apart.)
 Plan make_plan(const KvView &c, int n_q, int H, int k, int n_draft) {
   Plan p;
   const int G = H / c.H_kv;

@@ -22,13 +22,17 @@
 // the SM's share of HBM.  What decides is the MMA thread: an instruction costs
 // it 65 to 85 cycles, a commit or a wait 70, so S is issued at N = 128 for
 // both sets (24 queries x 4 heads over 32K bf16 tokens of 4 sequences, 8
-// key/value heads: 98 us, 5.5 TB/s; 143 us with chunks of 64).  128 CTAs are
-// one wave there; a chunk takes 1.3 us, the beginning, the end and the join
-// about 15 us.  e4m3 rows have half the bytes but take 145 us: a softmax thread
-// weighs its 64 tokens in 2200 cycles there (1300 for bf16), of which its
-// exponentials are 1000 (two warps on a scheduler's special-function unit), the
-// rest are the tokens' scales and latencies; the widening keeps up (eight
-// producer warps, at 96 registers, made it 160 us).
+// key/value heads: 96 us in bursts, 5.6 TB/s, and 107 in long runs at the card's
+// power limit; 143 us with chunks of 64).  128 CTAs are one wave there; a chunk
+// takes 1.3 us, the beginning, the end and the join about 15 us.  e4m3 rows have
+// half the bytes but take 145 us.  A chunk takes 4200 cycles there, of every
+// role: 2200 are a softmax thread's weighing of its 64 tokens (1300 for bf16;
+// its exponentials are 1000, two warps on a scheduler's special-function unit),
+// the MMA thread waits 1900 for the weights, and what the softmax turn spends
+// outside the weighing is not resolved (captured over 8K tokens: issue slots 29 %
+// busy; of a warp's stalls per issue 1.7 are short scoreboard, 1.6 instructions
+// that have not arrived).  The widening keeps up (eight producer warps, at 96 registers,
+// made it 160 us).
 #include <type_traits>
 
 #include "attend.cuh"

@@ -11,13 +11,14 @@
 // in between.  A thread keeps its 8 pairs' cos and sin for the heads of a
 // token that it takes one after the other.
 //
-// Measured, 8 key/value heads of 128.  Write of 2 x 8192 rotated tokens to e4m3
-// (102 MB): 26.6 us, 3.8 TB/s (28.7 with codes taken at both ends of an interval
-// around the quotient and an fp64 product where they differed).  Read of 8 x 2048
-// listed e4m3 tokens (102 MB with the outputs): 20.7 us, 4.9 TB/s; forms with
-// fewer instructions (row numbers by multiplication, paired products) and with
-// two pieces per thread took 21.2 to 22.6.  A few rows: 4.1 us either way, the
-// launch and its dependent loads.
+// Measured, 8 key/value heads of 128, a call in a row of them / alone in a graph.
+// Write of 2 x 8192 rotated tokens to e4m3 (102 MB): 24.2 us, 4.2 TB/s / 26.6 (28.7
+// with codes taken at both ends of an interval around the quotient and an fp64
+// product where they differed).  Read of 8 x 2048 listed e4m3 tokens (102 MB with
+// the outputs): 19.1 us, 5.3 TB/s / 20.7; forms with fewer instructions (row
+// numbers by multiplication, paired products) and with two pieces per thread took
+// 21.2 to 22.6 alone.  A few rows: 2.4 / 4.1 us either way, the launch and its
+// dependent loads.
 #include <algorithm>
 
 #include "attention.h"
