@@ -248,8 +248,14 @@ def workspace_bytes(op: int, cache: KeyCache, qs: Queries, h: int = 0, k: int = 
 def _ws(ws: Optional[Workspace], nbytes: int, device, stream):
     if nbytes == 0:
         return None, 0
-    ws = ws or Workspace(device)
-    return ws.get(nbytes, stream), nbytes
+    if ws is not None:
+        return ws.get(nbytes, stream), nbytes
+    buf = Workspace(device).get(nbytes, stream)
+    if stream is not None and buf.is_cuda:
+        # not handed out again before the call, on another stream than the one it belongs to, is done with it
+        stream = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+        buf.record_stream(stream)
+    return buf, nbytes
 
 
 def pool_keys(cache: KeyCache, new_keys: Optional[torch.Tensor] = None, new_scale: Optional[torch.Tensor] = None,

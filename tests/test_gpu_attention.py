@@ -987,6 +987,38 @@ def test_workspaces_keep_what_others_may_still_use():
     assert sum(b.numel() for b in ws.outgrown) <= 2 * ws.buf.numel()
 
 
+def test_a_call_on_another_stream_keeps_its_own_workspace(monkeypatch):
+    """Scratch that a call allocates for itself is not handed out again while the call waits on its stream."""
+    from long_context_misa_b200 import inputs as G
+    inp = G.make_inputs(G.WORKLOADS["tiny_decode"], 0)
+    cache, qs = M.device_inputs(inp)
+    M.pool_keys(cache)
+    heads = M.route_heads(cache, qs, 8)
+    want = M.score_topk(cache, qs, heads, 256)
+    had = []
+    get = M.Workspace.get
+
+    def noted(self, nbytes, stream=None):
+        buf = get(self, nbytes, stream)
+        had.append((buf.data_ptr(), buf.numel()))
+        return buf
+    monkeypatch.setattr(M.Workspace, "get", noted)
+    side = torch.cuda.Stream()
+    top = torch.empty_like(want)
+    torch.cuda.synchronize()
+    for given in (side, side.cuda_stream):
+        had.clear()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)              # about 10 ms in which the call cannot start
+        M.score_topk(cache, qs, heads, 256, topk=top, stream=given)
+        for at, size in had:
+            x = torch.empty(size, dtype=torch.uint8, device=DEV)
+            assert x.data_ptr() != at
+            x.fill_(255)
+        side.synchronize()
+        assert had and torch.equal(top, want)
+
+
 def test_same_call_same_bits():
     c = Case(False, 128, 4, 4, lens=(30000, 777), per=(3, 2), seed=52)
     a = c.run()
